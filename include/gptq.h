@@ -58,7 +58,8 @@ typedef enum gptq_status {
     GPTQ_ERR_UNSUPPORTED = -8   /* current device is not compute capability 10.0 */
 } gptq_status;
 
-enum { GPTQ_DTYPE_F16 = 0, GPTQ_DTYPE_F32 = 1 };
+/* GPTQ_DTYPE_BF16 is accepted by the fp8_* and kv_cache_* calls only. */
+enum { GPTQ_DTYPE_F16 = 0, GPTQ_DTYPE_F32 = 1, GPTQ_DTYPE_BF16 = 2 };
 
 /* Human-readable name of a status code (static string). */
 const char* gptq_status_string(int status);
@@ -377,6 +378,105 @@ gptq_status gptq_rms_norm(const void* X, int64_t n_tokens, int d, float eps, voi
  *   A   device fp16 [n_tokens x d_ff].   d_ff: a multiple of 8; both 16-byte aligned.
  * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
 gptq_status gptq_silu_mul(const void* GU, int64_t n_tokens, int d_ff, void* A, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The 8-bit floating-point layer (W8A8): e4m3 codes of the weights with one fp32 scale per
+ * 128 x 128 block, e4m3 codes of the activations with one fp32 scale per token and 128
+ * channels, and their product with fp32 accumulation. It stands beside the W4A16 layer for
+ * projections that keep 8 bits and have the tensor cores' 8-bit rate to win.
+ *   e4m3: 4 exponent and 3 fraction bits, largest magnitude 448, no infinities, code 0x7F NaN.
+ *   A block's scale and codes: a = max(max|x|, 2^-100), s = a / 448, r = 448 / a (both fp32
+ *   divisions), code = e4m3(x * r): the fp32 product rounded to nearest, halves to even. A block
+ *   that holds a NaN or an infinity gets s = NaN and NaN codes, so what is computed from it is NaN.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Codes and scales of activations.
+ *   X        device [n_tokens x d], fp16, fp32 or bf16 (x_dtype), 16-byte aligned; n_tokens >= 0
+ *            (0 is a no-op), below 2^31.   d: a multiple of 16, <= 65536.
+ *   codes    device uint8 [n_tokens x d] (e4m3), 16-byte aligned.
+ *   scales   device fp32 [ceil(d/128) x n_tokens]: scales[b][t] of token t's channels 128b..128b+127
+ *            (the last block may be narrower).
+ * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+gptq_status fp8_quantize_act(const void* X, int x_dtype, int64_t n_tokens, int d, uint8_t* codes,
+                             float* scales, void* stream);
+
+/* Codes and scales of a weight matrix.
+ *   W        device [d_out x d_in], fp16, fp32 or bf16, 16-byte aligned.   d_out >= 1.
+ *            d_in: a multiple of 16, <= 65536.
+ *   codes    device uint8 [d_out x d_in] (e4m3), 16-byte aligned.
+ *   scales   device fp32 [ceil(d_out/128) x ceil(d_in/128)] (the last blocks may be smaller).
+ * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+gptq_status fp8_quantize_weight(const void* W, int w_dtype, int d_out, int d_in, uint8_t* codes,
+                                float* scales, void* stream);
+
+/* Y[t][o] = sum over 128-channel blocks b of x_scales[b][t] * w_scales[o/128][b] *
+ *           (sum over the block's channels of X8[t][c] * W8[o][c])  + R[t][o],
+ * the block's inner sum on the tensor cores from zero, the sum over blocks in fp32 with
+ * round-to-nearest, one rounding to Y's type.
+ *   X8, x_scales   as fp8_quantize_act writes them; 0 <= n_tokens < 2^31 (0 is a no-op).
+ *   W8, w_scales   as fp8_quantize_weight writes them.   d_in: a multiple of 16, <= 65536.
+ *                  d_out >= 1.
+ *   R        device, Y's type, [n_tokens x d_out], or NULL (a residual added in fp32 before the
+ *            rounding; may be the same buffer as Y).
+ *   Y        device [n_tokens x d_out], fp16, fp32 or bf16 (y_dtype).
+ *            X8, W8, Y and R 16-byte aligned.
+ *   status_dev device int or NULL: set to GPTQ_ERR_TIMEOUT if a bounded wait gave up.
+ * Asynchronous; equal inputs give equal bits. Errors: ARG, CUDA, UNSUPPORTED. */
+gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int64_t n_tokens, int d_in,
+                       const uint8_t* W8, const float* w_scales, int d_out, const void* R, void* Y,
+                       int y_dtype, int* status_dev, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The quantised key/value cache: the group min-max quantizer of rtn_minmax_quantize applied to
+ * keys and values as they are written, per token and head, in groups of group_size
+ * consecutive elements of head_dim. Per group: the range widened to contain 0, scale =
+ * (max - min)/(2^bits - 1) rounded up to fp16 (1 for an all-zero group), zero = rint(-min/scale),
+ * code = clamp(rint(x/scale) + zero, 0, 2^bits - 1); bit-exact with that definition in fp64. A
+ * group that holds a NaN or an infinity, or whose scale exceeds fp16's range, stores scale NaN,
+ * zero 0 and codes 0, and reads back as NaN.
+ * The cache is paged. Its three arrays are the caller's:
+ *   codes    device uint8 [2 x n_pages x page_size x n_heads x head_dim*bits/8]: keys, then values;
+ *            bits == 4: two codes per byte, the even element in the low nibble. 16-byte aligned.
+ *   scales, zeros  device fp16 [2 x n_pages x page_size x n_heads x head_dim/group_size].
+ * A slot is page * page_size + place in the page.
+ *   bits 4 or 8.   group_size 16, 32, 64, 128 or 256, dividing head_dim.   n_heads >= 1;
+ *   n_heads * head_dim <= 65536.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Quantise and write n_tokens tokens.
+ *   K, V     device, fp16, fp32 or bf16: token t's [n_heads x head_dim] keys start at element
+ *            t * k_stride, its values at t * v_stride (strides >= 0, multiples of 16 bytes: views
+ *            of a fused projection's output need no copy). 16-byte aligned.
+ *   slots    device int64 [n_tokens]: each token's slot. A negative slot skips the token. Slots of
+ *            one call must be distinct: a slot given twice ends with unspecified contents (no
+ *            other slot is touched).
+ *   n_slots  n_pages * page_size of the cache.
+ *   status_dev device int or NULL: set to GPTQ_ERR_ARG if a slot is >= n_slots (that token is
+ *            skipped).
+ * Only the named slots change. Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+gptq_status kv_cache_write(const void* K, const void* V, int dtype, int64_t n_tokens,
+                           int64_t k_stride, int64_t v_stride, int n_heads, int head_dim,
+                           const int64_t* slots, int64_t n_slots, int bits, int group_size,
+                           uint8_t* codes, uint16_t* scales, uint16_t* zeros, int* status_dev,
+                           void* stream);
+
+/* Read the context of n_seqs sequences back, packed one after the other:
+ * K[t], V[t] = out_type(scale * (code - zero)) (one rounding) of position t - cu_lens[b] of the
+ * sequence b with cu_lens[b] <= t < cu_lens[b+1].
+ *   page_table device int32 [n_seqs x max_pages]: the page of a sequence's positions
+ *            j*page_size .. is entry j. Entries behind a sequence's last page are not read.
+ *   cu_lens  device int32 [n_seqs + 1], ascending: running sums of the lengths (0 allowed).
+ *   total    rows of K and V, >= 0. Rows from cu_lens[n_seqs] on (and before cu_lens[0]) are left
+ *            as they were.
+ *   K, V     device [total x n_heads x head_dim], fp16, fp32 or bf16 (dtype), 16-byte aligned.
+ *   status_dev device int or NULL: set to GPTQ_ERR_ARG if a position is behind max_pages pages or
+ *            a page is outside 0 .. n_pages - 1 (such rows are written as zeros).
+ * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+gptq_status kv_cache_read(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros,
+                          int64_t n_pages, int page_size, int n_heads, int head_dim, int bits,
+                          int group_size, const int32_t* page_table, int n_seqs, int max_pages,
+                          const int32_t* cu_lens, int64_t total, void* K, void* V, int dtype,
+                          int* status_dev, void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * Stage timing. When enabled, gptq_quantize_layer records CUDA events around each stage on

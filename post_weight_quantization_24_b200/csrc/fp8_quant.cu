@@ -1,0 +1,209 @@
+// e4m3 codes with one fp32 scale per block of 128: activations per token and 128 channels,
+// weights per 128 x 128 block.
+//
+// a = max(max|x|, 2^-100), s = a/448, r = 448/a, code = e4m3(x*r). 448 is e4m3's largest
+// magnitude, so the block's largest value lands on the top code; the floor keeps s and r normal
+// fp32 numbers for every input (an all-zero block gets s = 2^-100/448 and zero codes).
+// max|x| is taken over integer magnitudes, which carries NaN and infinity along: such a block
+// gets s = r = NaN and NaN codes.
+//
+// Both kernels read X once into registers and write its codes from there: bytes per value are
+// the input's 2 or 4 plus 1, plus the scales. They are bound by HBM.
+#include <algorithm>
+
+#include "internal.cuh"
+#include "vec.cuh"
+
+namespace gq {
+
+constexpr float kE4m3Max = 448.0f;
+
+struct Fp8Scale {
+    float s, r;
+};
+
+__device__ __forceinline__ Fp8Scale fp8_scale(uint32_t amax_bits) {
+    const float a = amax_bits >= kInfBits ? __uint_as_float(0x7FC00000u)
+                                          : fmaxf(__uint_as_float(amax_bits), 0x1p-100f);
+    return {__fdiv_rn(a, kE4m3Max), __fdiv_rn(kE4m3Max, a)};
+}
+
+// two products to two e4m3 codes, the first in the low byte (|x*r| <= 448 up to a rounding)
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t o;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(o) : "f"(hi), "f"(lo));
+    return o;
+}
+
+// one 16-byte vector's codes: 8 bytes (fp16, bf16) or 4 (fp32)
+template <typename T>
+__device__ __forceinline__ void store_codes_vec(uint8_t* p, const uint4& u, float r) {
+    float v[Vec<T>::N];
+    Vec<T>::unpack(u, v);
+    uint32_t w[Vec<T>::N / 4];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N / 4; ++i)
+        w[i] = e4m3x2(v[4 * i] * r, v[4 * i + 1] * r) |
+               (e4m3x2(v[4 * i + 2] * r, v[4 * i + 3] * r) << 16);
+    if constexpr (Vec<T>::N == 8)
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t amax_vec(const uint4& u, uint32_t m) {
+    float v[Vec<T>::N];
+    Vec<T>::unpack(u, v);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) m = max(m, abs_bits(v[i]));
+    return m;
+}
+
+// A warp takes 4 tokens x 128 channels: 8 lanes per token, each with C vectors 8*N channels
+// apart, so that every load and store of 8 lanes is one contiguous run.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, int64_t n, int d,
+                                                      uint8_t* __restrict__ codes,
+                                                      float* __restrict__ scales) {
+    constexpr int N = Vec<T>::N, C = 128 / (8 * N);
+    const int lane = lane_id(), part = lane & 7;
+    const int nb = (d + 127) / 128;
+    const int64_t n_rb = (n + 31) / 32, units = n_rb * nb;     // 32 tokens x 128 channels
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t rb = u / nb;
+        const int b = static_cast<int>(u - rb * nb);
+        const int64_t t = rb * 32 + warp_id() * 4 + (lane >> 3);
+        uint4 x[C];
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = b * 128 + (c * 8 + part) * N;
+            x[c] = make_uint4(0, 0, 0, 0);
+            if (t < n && k < d) x[c] = __ldg(reinterpret_cast<const uint4*>(X + t * d + k));
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) m = amax_vec<T>(x[c], m);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const Fp8Scale f = fp8_scale(m);
+        if (t >= n) continue;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = b * 128 + (c * 8 + part) * N;
+            if (k < d) store_codes_vec<T>(codes + t * d + k, x[c], f.r);
+        }
+        if (part == 0) scales[b * n + t] = f.s;
+    }
+}
+
+// A block of 256 threads takes one 128 x 128 block: 8 lanes per row, 4 rows per warp and step.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_weight_kernel(const T* __restrict__ W, int d_out,
+                                                         int d_in, uint8_t* __restrict__ codes,
+                                                         float* __restrict__ scales) {
+    constexpr int N = Vec<T>::N, C = 128 / (8 * N);
+    __shared__ uint32_t warp_max[8];
+    const int lane = lane_id(), part = lane & 7;
+    const int nb = (d_in + 127) / 128;
+    const int64_t rb = blockIdx.x / nb;
+    const int b = static_cast<int>(blockIdx.x - rb * nb);
+    uint4 x[4][C];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t row = rb * 128 + j * 32 + warp_id() * 4 + (lane >> 3);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = b * 128 + (c * 8 + part) * N;
+            x[j][c] = make_uint4(0, 0, 0, 0);
+            if (row < d_out && k < d_in)
+                x[j][c] = __ldg(reinterpret_cast<const uint4*>(W + row * d_in + k));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int c = 0; c < C; ++c) m = amax_vec<T>(x[j][c], m);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) warp_max[warp_id()] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = max(m, warp_max[w]);
+    const Fp8Scale f = fp8_scale(m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t row = rb * 128 + j * 32 + warp_id() * 4 + (lane >> 3);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = b * 128 + (c * 8 + part) * N;
+            if (row < d_out && k < d_in) store_codes_vec<T>(codes + row * d_in + k, x[j][c], f.r);
+        }
+    }
+    if (threadIdx.x == 0) scales[blockIdx.x] = f.s;
+}
+
+template <typename T>
+static gptq_status fp8_act_launch(const void* X, int64_t n, int d, uint8_t* codes, float* scales,
+                                  cudaStream_t s) {
+    const int64_t units = ((n + 31) / 32) * ((d + 127) / 128);
+    const int grid = static_cast<int>(std::min<int64_t>(units, int64_t(1) << 30));
+    fp8_act_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(X), n, d, codes, scales);
+    GPTQ_LAUNCHED();
+    return GPTQ_OK;
+}
+
+template <typename T>
+static gptq_status fp8_weight_launch(const void* W, int d_out, int d_in, uint8_t* codes,
+                                     float* scales, cudaStream_t s) {
+    // at most 2^24 row blocks x 512 column blocks
+    const int64_t blocks = ((static_cast<int64_t>(d_out) + 127) / 128) * ((d_in + 127) / 128);
+    if (blocks > 0x7FFFFFFF) return GPTQ_ERR_ARG;
+    fp8_weight_kernel<T><<<static_cast<int>(blocks), 256, 0, s>>>(static_cast<const T*>(W), d_out,
+                                                                  d_in, codes, scales);
+    GPTQ_LAUNCHED();
+    return GPTQ_OK;
+}
+
+static bool fp8_dtype_ok(int t) {
+    return t == GPTQ_DTYPE_F16 || t == GPTQ_DTYPE_F32 || t == GPTQ_DTYPE_BF16;
+}
+static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+static bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+}  // namespace gq
+
+extern "C" {
+
+gptq_status fp8_quantize_act(const void* X, int x_dtype, int64_t n_tokens, int d, uint8_t* codes,
+                             float* scales, void* stream) {
+    if (!gq::fp8_dtype_ok(x_dtype) || n_tokens < 0 || n_tokens >= (int64_t(1) << 31))
+        return GPTQ_ERR_ARG;
+    if (d < 16 || d % 16 || d > 65536) return GPTQ_ERR_ARG;
+    if (n_tokens == 0) return GPTQ_OK;
+    if (!X || !codes || !scales || !gq::al16(X) || !gq::al16(codes) || !gq::al4(scales))
+        return GPTQ_ERR_ARG;
+    GPTQ_TRY(gq::check_device());
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (x_dtype) {
+        case GPTQ_DTYPE_F16: return gq::fp8_act_launch<__half>(X, n_tokens, d, codes, scales, s);
+        case GPTQ_DTYPE_BF16: return gq::fp8_act_launch<__nv_bfloat16>(X, n_tokens, d, codes, scales, s);
+        default: return gq::fp8_act_launch<float>(X, n_tokens, d, codes, scales, s);
+    }
+}
+
+gptq_status fp8_quantize_weight(const void* W, int w_dtype, int d_out, int d_in, uint8_t* codes,
+                                float* scales, void* stream) {
+    if (!W || !codes || !scales || !gq::fp8_dtype_ok(w_dtype)) return GPTQ_ERR_ARG;
+    if (d_out < 1 || d_in < 16 || d_in % 16 || d_in > 65536) return GPTQ_ERR_ARG;
+    if (!gq::al16(W) || !gq::al16(codes) || !gq::al4(scales)) return GPTQ_ERR_ARG;
+    GPTQ_TRY(gq::check_device());
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (w_dtype) {
+        case GPTQ_DTYPE_F16: return gq::fp8_weight_launch<__half>(W, d_out, d_in, codes, scales, s);
+        case GPTQ_DTYPE_BF16: return gq::fp8_weight_launch<__nv_bfloat16>(W, d_out, d_in, codes, scales, s);
+        default: return gq::fp8_weight_launch<float>(W, d_out, d_in, codes, scales, s);
+    }
+}
+
+}  // extern "C"

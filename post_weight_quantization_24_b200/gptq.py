@@ -11,6 +11,10 @@ Functions (names follow the C ABI in ``include/gptq.h``):
   quantize_layer_workspace(...)    workspace bytes for quantize_layer
   inverse_factor(H, ...)           processing order and U with UᵀU = H_d⁻¹ (stage 2 alone)
   rtn_minmax_quantize(W, ...)      group min-max RTN -> packed codes, scales, zeros
+  fp8_quantize_act(X)              e4m3 codes, a scale per token and 128 channels
+  fp8_quantize_weight(W)           e4m3 codes, a scale per 128 x 128 block
+  fp8_linear(X8, sx, W8, sw, ...)  Y = X̂·Ŵᵀ (+ R) from those codes and scales
+  kv_cache_alloc / _write / _read  paged key/value cache of 4- or 8-bit codes
   profile_enable(on), profile_read()  per-stage milliseconds of the last quantize_layer call
 """
 
@@ -27,7 +31,7 @@ LIB_PATH = os.path.join(HERE, "libgptq_b200.so")
 STATUS = {0: "GPTQ_OK", -1: "GPTQ_ERR_ARG", -2: "GPTQ_ERR_NOT_PD", -3: "GPTQ_ERR_NONFINITE",
           -4: "GPTQ_ERR_CUDA", -5: "GPTQ_ERR_OOM", -6: "GPTQ_ERR_TIMEOUT",
           -7: "GPTQ_ERR_WORKSPACE", -8: "GPTQ_ERR_UNSUPPORTED"}
-DTYPE_F16, DTYPE_F32 = 0, 1
+DTYPE_F16, DTYPE_F32, DTYPE_BF16 = 0, 1, 2
 STAGES = ("prepare", "factor", "images", "column_loop", "lazy_update", "assemble", "loss")
 
 
@@ -80,6 +84,13 @@ _SIGNATURES = {
     "awq_lite_search": ([_P, _I, _I, _I, _P, _I64, _P, _I, _I, _I, ctypes.c_double, _P, _P, _P,
                          _P, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I), _P, _SZ, _P],
                         _I),
+    "fp8_quantize_act": ([_P, _I, _I64, _I, _P, _P, _P], _I),
+    "fp8_quantize_weight": ([_P, _I, _I, _I, _P, _P, _P], _I),
+    "fp8_linear": ([_P, _P, _I64, _I, _P, _P, _I, _P, _P, _I, _P, _P], _I),
+    "kv_cache_write": ([_P, _P, _I, _I64, _I64, _I64, _I, _I, _P, _I64, _I, _I, _P, _P, _P, _P,
+                        _P], _I),
+    "kv_cache_read": ([_P, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _I, _I, _P, _I64, _P, _P, _I,
+                       _P, _P], _I),
     "gptq_quantize_layer_noalloc": ([_P, _I, _I, _I, _P, _I, _I, _I, _F, _I, _P, _P, _P, _P, _P,
                                      ctypes.POINTER(_F), _P], _I),
     "gptq_profile_enable": ([_I], None),
@@ -471,6 +482,207 @@ def silu_mul(GU: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     _check(lib().gptq_silu_mul(GU.data_ptr(), n, two // 2, out.data_ptr(), _stream()),
            "gptq_silu_mul")
     return out
+
+
+# ------------------------------------------------------------------------------------------
+# 8-bit floating-point layer
+# ------------------------------------------------------------------------------------------
+_FLOAT_CODES = {torch.float16: DTYPE_F16, torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_E4M3 = torch.float8_e4m3fn
+
+
+def _float_code(dtype: torch.dtype, name: str) -> int:
+    code = _FLOAT_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float16, float32 or bfloat16, got {dtype}")
+    return code
+
+
+def _require(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=None) -> None:
+    """A contiguous tensor on the current CUDA device, of this type and shape."""
+    _require_cuda(t, name)
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _require_status(status: torch.Tensor | None) -> None:
+    if status is not None:
+        _require(status, "status", torch.int32)
+        if status.numel() < 1:
+            raise ValueError("status must hold an int32")
+
+
+def fp8_quantize_act(X: torch.Tensor, out: tuple | None = None):
+    """Activations X [n, d] (fp16/fp32/bf16, d a multiple of 16) -> (codes float8_e4m3fn [n, d],
+    scales fp32 [ceil(d/128), n]): one scale per token and 128 channels (see fp8_quantize_act in
+    include/gptq.h). ``out``: the two tensors to write."""
+    _require(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [n, d]")
+    n, d = X.shape
+    code = _float_code(X.dtype, "X")
+    nb = (d + 127) // 128
+    if out is None:
+        codes = torch.empty(n, d, dtype=_E4M3, device=X.device)
+        scales = torch.empty(nb, n, dtype=torch.float32, device=X.device)
+    else:
+        codes, scales = out
+        _require(codes, "codes", _E4M3, (n, d))
+        _require(scales, "scales", torch.float32, (nb, n))
+    _check(lib().fp8_quantize_act(X.data_ptr(), code, n, d, codes.data_ptr(), scales.data_ptr(),
+                                  _stream()), "fp8_quantize_act")
+    return codes, scales
+
+
+def fp8_quantize_weight(W: torch.Tensor, out: tuple | None = None):
+    """Weights W [d_out, d_in] (fp16/fp32/bf16, d_in a multiple of 16) -> (codes float8_e4m3fn
+    [d_out, d_in], scales fp32 [ceil(d_out/128), ceil(d_in/128)]): one scale per 128 x 128
+    block."""
+    _require(W, "W")
+    if W.dim() != 2:
+        raise ValueError("W must be [d_out, d_in]")
+    d_out, d_in = W.shape
+    code = _float_code(W.dtype, "W")
+    ns = ((d_out + 127) // 128, (d_in + 127) // 128)
+    if out is None:
+        codes = torch.empty(d_out, d_in, dtype=_E4M3, device=W.device)
+        scales = torch.empty(ns, dtype=torch.float32, device=W.device)
+    else:
+        codes, scales = out
+        _require(codes, "codes", _E4M3, (d_out, d_in))
+        _require(scales, "scales", torch.float32, ns)
+    _check(lib().fp8_quantize_weight(W.data_ptr(), code, d_out, d_in, codes.data_ptr(),
+                                     scales.data_ptr(), _stream()), "fp8_quantize_weight")
+    return codes, scales
+
+
+def fp8_linear(X8: torch.Tensor, x_scales: torch.Tensor, W8: torch.Tensor,
+               w_scales: torch.Tensor, R: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, dtype: torch.dtype = torch.float16,
+               status: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = X̂·Ŵᵀ + R [n, d_out] (fp16/fp32/bf16) from fp8_quantize_act's and
+    fp8_quantize_weight's codes and scales; R has Y's type and may be ``out``."""
+    _require(X8, "X8", _E4M3)
+    _require(W8, "W8", _E4M3)
+    if X8.dim() != 2 or W8.dim() != 2 or X8.shape[1] != W8.shape[1]:
+        raise ValueError("X8 must be [n, d_in] and W8 [d_out, d_in]")
+    n, d_in = X8.shape
+    d_out = W8.shape[0]
+    nb = (d_in + 127) // 128
+    _require(x_scales, "x_scales", torch.float32, (nb, n))
+    _require(w_scales, "w_scales", torch.float32, ((d_out + 127) // 128, nb))
+    if out is None:
+        code = _float_code(dtype, "dtype")
+        out = torch.empty(n, d_out, dtype=dtype, device=X8.device)
+    else:
+        _require(out, "out", None, (n, d_out))
+        code = _float_code(out.dtype, "out")
+    if R is not None:
+        _require(R, "R", out.dtype, (n, d_out))
+    _require_status(status)
+    _check(lib().fp8_linear(X8.data_ptr(), x_scales.data_ptr(), n, d_in, W8.data_ptr(),
+                            w_scales.data_ptr(), d_out, _ptr(R), out.data_ptr(), code,
+                            _ptr(status), _stream()), "fp8_linear")
+    return out
+
+
+# ------------------------------------------------------------------------------------------
+# quantised key/value cache
+# ------------------------------------------------------------------------------------------
+def kv_cache_alloc(n_pages: int, page_size: int, n_heads: int, head_dim: int, bits: int = 8,
+                   group_size: int = 64, device="cuda"):
+    """The three arrays of an empty cache: codes uint8 [2, n_pages, page_size, n_heads,
+    head_dim*bits/8], scales and zeros fp16 [2, n_pages, page_size, n_heads,
+    head_dim/group_size] (keys, then values). A slot that was never written reads as zeros."""
+    if bits not in (4, 8) or group_size < 1 or head_dim % group_size:
+        raise ValueError("bits must be 4 or 8 and group_size divide head_dim")
+    shape = (2, n_pages, page_size, n_heads)
+    codes = torch.zeros(*shape, head_dim * bits // 8, dtype=torch.uint8, device=device)
+    scales = torch.zeros(*shape, head_dim // group_size, dtype=torch.float16, device=device)
+    return codes, scales, torch.zeros_like(scales)
+
+
+def _cache_dims(codes, scales, zeros, bits):
+    """(n_pages, page_size, n_heads, head_dim, group_size) of a cache's arrays, checked."""
+    _require(codes, "codes", torch.uint8)
+    if codes.dim() != 5 or codes.shape[0] != 2 or bits not in (4, 8) or codes.shape[4] < 1:
+        raise ValueError("codes must be [2, n_pages, page_size, n_heads, head_dim*bits/8], bits 4 or 8")
+    _, n_pages, page_size, n_heads, row = codes.shape
+    head_dim = row * 8 // bits
+    if scales.dim() != 5 or scales.shape[4] < 1 or head_dim % scales.shape[4]:
+        raise ValueError("scales must be [2, n_pages, page_size, n_heads, head_dim/group_size]")
+    shape = codes.shape[:4] + scales.shape[4:]
+    _require(scales, "scales", torch.float16, shape)
+    _require(zeros, "zeros", torch.float16, shape)
+    return n_pages, page_size, n_heads, head_dim, head_dim // scales.shape[4]
+
+
+def _token_stride(t: torch.Tensor, name: str, n_heads: int, head_dim: int) -> int:
+    """Elements from a token's row to the next; the row itself is contiguous."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dim() != 3 or t.shape[1:] != (n_heads, head_dim):
+        raise ValueError(f"{name} must be [n, {n_heads}, {head_dim}]")
+    st = t.stride()
+    if t.numel() and (st[2] != 1 or (n_heads > 1 and st[1] != head_dim)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return st[0] if t.shape[0] > 1 else n_heads * head_dim
+
+
+def kv_cache_write(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, codes: torch.Tensor,
+                   scales: torch.Tensor, zeros: torch.Tensor, bits: int = 8,
+                   status: torch.Tensor | None = None) -> None:
+    """Quantise K, V [n, n_heads, head_dim] (fp16/fp32/bf16; rows may lie apart, as in a fused
+    projection's output) into the cache's slots [n] int64 (page * page_size + place; negative:
+    skipped; distinct). A slot behind the cache is skipped and sets ``status`` to
+    GPTQ_ERR_ARG."""
+    n_pages, page_size, H, D, g = _cache_dims(codes, scales, zeros, bits)
+    ks, vs = _token_stride(K, "K", H, D), _token_stride(V, "V", H, D)
+    code = _float_code(K.dtype, "K")
+    if V.dtype != K.dtype or V.shape != K.shape:
+        raise ValueError("V must have K's type and shape")
+    n = K.shape[0]
+    _require(slots, "slots", torch.int64, (n,))
+    _require_status(status)
+    _check(lib().kv_cache_write(K.data_ptr(), V.data_ptr(), code, n, ks, vs, H, D,
+                                slots.data_ptr(), n_pages * page_size, bits, g, codes.data_ptr(),
+                                scales.data_ptr(), zeros.data_ptr(), _ptr(status), _stream()),
+           "kv_cache_write")
+
+
+def kv_cache_read(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                  page_table: torch.Tensor, cu_lens: torch.Tensor, total: int, bits: int = 8,
+                  dtype: torch.dtype = torch.float16, out: tuple | None = None,
+                  status: torch.Tensor | None = None):
+    """The context of every sequence, packed: (K, V) [total, n_heads, head_dim] of positions
+    0 .. len-1 of each sequence in turn. page_table int32 [n_seqs, max_pages], cu_lens int32
+    [n_seqs + 1] (running sums of the lengths). Rows behind cu_lens[-1] are left as they were;
+    positions without a page of the cache come as zeros and set ``status`` to GPTQ_ERR_ARG."""
+    n_pages, page_size, H, D, g = _cache_dims(codes, scales, zeros, bits)
+    _require(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seqs, max_pages]")
+    n_seqs, max_pages = page_table.shape
+    _require(cu_lens, "cu_lens", torch.int32, (n_seqs + 1,))
+    if out is None:
+        code = _float_code(dtype, "dtype")
+        K = torch.empty(total, H, D, dtype=dtype, device=codes.device)
+        V = torch.empty(total, H, D, dtype=dtype, device=codes.device)
+    else:
+        K, V = out
+        code = _float_code(K.dtype, "K")
+        _require(K, "K", None, (total, H, D))
+        _require(V, "V", K.dtype, (total, H, D))
+    _require_status(status)
+    _check(lib().kv_cache_read(codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), n_pages,
+                               page_size, H, D, bits, g, page_table.data_ptr(), n_seqs, max_pages,
+                               cu_lens.data_ptr(), total, K.data_ptr(), V.data_ptr(), code,
+                               _ptr(status), _stream()), "kv_cache_read")
+    return K, V
 
 
 # ------------------------------------------------------------------------------------------
