@@ -48,18 +48,20 @@ struct F8Params {
 
 // Tiles run in bands of 8 token tiles with the token tile varying fastest, so the CTAs that run
 // together share weight tiles and activation rows in L2.
-__device__ __forceinline__ void f8_tile(const F8Params& p, long long t, int& m0, int& n0) {
+__device__ __forceinline__ void f8_tile(const F8Params& p, long long t, int bm, int bn, int& m0,
+                                        int& n0) {
     const long long per_band = static_cast<long long>(f8::BAND) * p.n_nt;
     const int band = static_cast<int>(t / per_band);
     const int rem = static_cast<int>(t - band * per_band);
     const int band_m = min(f8::BAND, p.n_mt - band * f8::BAND);
-    m0 = (band * f8::BAND + rem % band_m) * f8::BM;
-    n0 = (rem / band_m) * f8::BN;
+    m0 = (band * f8::BAND + rem % band_m) * bm;
+    n0 = (rem / band_m) * bn;
 }
 
 // NC accumulated columns of one row -> Y (+ R), columns col0 .. min(col0 + NC, d_out)
 template <typename T, int NC>
-__device__ __forceinline__ void f8_store(const F8Params& p, int row, int col0, const float* acc) {
+__device__ __forceinline__ void f8_store(const F8Params& p, int row, int col0,
+                                         const uint64_t (&acc)[NC / 2]) {
     constexpr int N = Vec<T>::N;
     if (row >= p.n_tok || col0 >= p.d_out) return;
     const int64_t off = static_cast<int64_t>(row) * p.d_out + col0;
@@ -72,7 +74,7 @@ __device__ __forceinline__ void f8_store(const F8Params& p, int row, int col0, c
             if (c >= left) break;
             float v[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = acc[c + e];
+            for (int e = 0; e < N; ++e) v[e] = f32x2_get(acc[(c + e) / 2], e & 1);
             if (r) {
                 float f[N];
                 Vec<T>::unpack(*reinterpret_cast<const uint4*>(r + c), f);
@@ -85,9 +87,27 @@ __device__ __forceinline__ void f8_store(const F8Params& p, int row, int col0, c
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             if (c < left)
-                y[c] = Vec<T>::from_float(acc[c] + (r ? Vec<T>::to_float(r[c]) : 0.0f));
+                y[c] = Vec<T>::from_float(f32x2_get(acc[c / 2], c & 1) +
+                                          (r ? Vec<T>::to_float(r[c]) : 0.0f));
         }
     }
+}
+
+// acc += f * (NC/2 pairs of partial sums)
+template <int NC>
+__device__ __forceinline__ void f8_promote(uint64_t* acc, const uint32_t (&r)[NC], uint64_t f) {
+#pragma unroll
+    for (int k = 0; k < NC / 2; ++k) fma_f32x2(acc[k], f32x2(r[2 * k], r[2 * k + 1]), f);
+}
+
+// Wait of a whole warp, every lane on the barrier itself: true if it completed, else the timeout
+// is recorded.
+__device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, int* status,
+                                             volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_wait(bar, parity))) return true;
+    set_status(status, GPTQ_ERR_TIMEOUT);
+    *abort_flag = 1;
+    return false;
 }
 
 template <typename T>
@@ -135,7 +155,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
             int it = 0;
             for (long long t = blockIdx.x; t < p.n_tiles && !*abort_flag; t += gridDim.x) {
                 int m0, n0;
-                f8_tile(p, t, m0, n0);
+                f8_tile(p, t, f8::BM, f8::BN, m0, n0);
                 for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
                     const int st = it % f8::STAGES;
                     if (!mbar_wait(&empty[st], ((it / f8::STAGES) & 1) ^ 1)) {
@@ -199,24 +219,22 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
         bool stop = false;
         for (long long t = blockIdx.x; t < p.n_tiles && !stop; t += gridDim.x) {
             int m0, n0;
-            f8_tile(p, t, m0, n0);
+            f8_tile(p, t, f8::BM, f8::BN, m0, n0);
             const int row = m0 + 32 * q + lane;
             const float* sx = p.sx + min(row, p.n_tok - 1);
             const float* sw = p.sw + static_cast<int64_t>(n0 / 128) * p.n_kb;
-            float acc[f8::EPI_COLS];
+            uint64_t acc[f8::EPI_COLS / 2];
 #pragma unroll
-            for (int k = 0; k < f8::EPI_COLS; ++k) acc[k] = 0.0f;
+            for (int k = 0; k < f8::EPI_COLS / 2; ++k) acc[k] = 0;
+            float sx_next = __ldg(sx), sw_next = __ldg(sw);
             for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
                 const int b = it % f8::ACCS;
-                const float f = __ldg(sx + static_cast<int64_t>(kb) * p.n_tok) * __ldg(sw + kb);
-                int ok = 1;
-                if (lane == 0) ok = mbar_wait(&acc_full[b], (it / f8::ACCS) & 1) ? 1 : 0;
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok || __shfl_sync(0xffffffffu, *abort_flag, 0)) {
-                    if (lane == 0 && !ok) {
-                        set_status(p.status, GPTQ_ERR_TIMEOUT);
-                        *abort_flag = 1;
-                    }
+                const uint32_t f = __float_as_uint(sx_next * sw_next);
+                if (kb + 1 < p.n_kb) {
+                    sx_next = __ldg(sx + static_cast<int64_t>(kb + 1) * p.n_tok);
+                    sw_next = __ldg(sw + kb + 1);
+                }
+                if (!f8_warp_wait(&acc_full[b], (it / f8::ACCS) & 1, p.status, abort_flag)) {
                     stop = true;
                     break;
                 }
@@ -233,10 +251,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[b]);
 #pragma unroll
-                for (int j = 0; j < f8::EPI_COLS / 32; ++j)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        acc[32 * j + k] = fmaf(__uint_as_float(r[j][k]), f, acc[32 * j + k]);
+                for (int j = 0; j < f8::EPI_COLS / 32; ++j) f8_promote<32>(acc + 16 * j, r[j], f32x2(f, f));
             }
             if (!stop) f8_store<T, f8::EPI_COLS>(p, row, n0 + f8::EPI_COLS * half, acc);
         }
@@ -254,7 +269,6 @@ static gptq_status fp8_gemm_launch(const uint8_t* X8, const uint8_t* W8, F8Param
                                    cudaStream_t s) {
     GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<T>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, f8::SMEM));
-    p.vec_ok = p.d_out % Vec<T>::N == 0;
     CUtensorMap xmap, wmap;
     GPTQ_TRY(encode_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(X8),
                                   p.d_in, p.n_tok, p.d_in, f8::BK, f8::BM,
@@ -269,6 +283,257 @@ static gptq_status fp8_gemm_launch(const uint8_t* X8, const uint8_t* W8, F8Param
     fp8_gemm_kernel<T><<<grid, f8::THREADS, f8::SMEM, s>>>(xmap, wmap, p);
     GPTQ_LAUNCHED();
     return GPTQ_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// Pair kernel for large calls: two CTAs of a cluster share one 256 x 256 tile (tcgen05
+// cta_group::2, M256 N256 K32). Each CTA loads its 128 tokens and its 128 of the tile's 256
+// channels per block, 32 KB for 8.4 M products instead of the 64 KB that four 128 x 128 tiles
+// need, and promotes its own 128 tokens x 256 channels. Synchronisation as in the Hessian's pair
+// kernel: both CTAs' bytes complete on the leader's stage barrier, the leader's commits arrive on
+// both CTAs' barriers, both CTAs' promotion warps release an accumulator on the leader's.
+// ---------------------------------------------------------------------------------------
+namespace f8p {
+constexpr int PT = 256;                              // pair tile edge
+constexpr int BM = 128, BNC = 128;                   // tokens, channels loaded per CTA
+constexpr int BK = 128, STAGES = 6;
+constexpr int A_BYTES = BM * BK, STAGE = A_BYTES + BNC * BK;
+// Warpgroup 0 holds the producer and the issuer, warpgroups 1 and 2 promote: a thread keeps one
+// token's 128 sums and two 32-column loads in flight, more than an even share of registers.
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, EPI_COLS = 128;
+constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+constexpr int REGS = 168, REGS_IO = 56, REGS_EPI = 224;
+static_assert(REGS_IO * 128 + REGS_EPI * 256 <= REGS * THREADS, "register shares");
+constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+constexpr uint32_t TMEM_COLS = 512;                  // two accumulators of 256 columns
+constexpr uint32_t IDESC = umma_idesc_e4m3(PT, PT);
+static_assert(SMEM <= 227 * 1024, "shared memory");
+}  // namespace f8p
+
+template <typename T>
+__global__ void __launch_bounds__(f8p::THREADS, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                    const F8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + f8p::STAGES * f8p::STAGE);
+    uint64_t* empty = full + f8p::STAGES;
+    uint64_t* acc_full = empty + f8p::STAGES;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drained = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = warp_id(), lane = lane_id();
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const long long cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < f8p::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 2 * f8p::EPI_WARPS);
+        }
+        mbar_init(drained, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&xmap);
+        tma_prefetch_desc(&wmap);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, f8p::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();     // both CTAs' barriers exist before either CTA signals the other's
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp < f8p::EPI_WARP0) {
+    regs_shrink<f8p::REGS_IO>();
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs) ----------------
+        if (lane == 0) {
+            int it = 0;
+            for (long long t = cluster; t < p.n_tiles && !*abort_flag; t += n_clusters) {
+                int m0, n0;
+                f8_tile(p, t, f8p::PT, f8p::PT, m0, n0);
+                m0 += f8p::BM * static_cast<int>(rank);
+                n0 += f8p::BNC * static_cast<int>(rank);
+                for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
+                    const int st = it % f8p::STAGES;
+                    if (!mbar_wait(&empty[st], ((it / f8p::STAGES) & 1) ^ 1)) {
+                        set_status(p.status, GPTQ_ERR_TIMEOUT);
+                        *abort_flag = 1;
+                        break;
+                    }
+                    uint8_t* sa = smem + st * f8p::STAGE;
+                    if (leader) mbar_arrive_expect_tx(&full[st], 2 * f8p::STAGE);
+                    const uint32_t fb = mapa_shared(smem_u32(&full[st]), 0);
+                    tma_load_2d_pair(sa, &xmap, fb, kb * f8p::BK, m0);
+                    tma_load_2d_pair(sa + f8p::A_BYTES, &wmap, fb, kb * f8p::BK, n0);
+                }
+            }
+            // the leader's stage barriers count both CTAs' bytes: once it has seen the last
+            // stages complete, no copy of either CTA is still writing shared memory
+            if (leader) {
+                const int n_tail = it < f8p::STAGES ? it : f8p::STAGES;
+                for (int k = it - n_tail; k < it; ++k) {
+                    if (!mbar_wait(&full[k % f8p::STAGES], (k / f8p::STAGES) & 1)) {
+                        set_status(p.status, GPTQ_ERR_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (leader) ----------------
+        if (leader && lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (long long t = cluster; ok && t < p.n_tiles && !*abort_flag; t += n_clusters) {
+                for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
+                    const int st = it % f8p::STAGES, b = it & 1;
+                    if (!mbar_wait(&full[st], (it / f8p::STAGES) & 1) ||
+                        !mbar_wait(&acc_empty[b], ((it >> 1) & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * f8p::PT);
+                    const uint32_t s0 = smem_u32(smem + st * f8p::STAGE);
+#pragma unroll
+                    for (int kk = 0; kk < f8p::BK / 32; ++kk) {
+                        const uint64_t ad = umma_desc_sw128(s0 + kk * 32, 16, 1024);
+                        const uint64_t bd = umma_desc_sw128(s0 + f8p::A_BYTES + kk * 32, 16, 1024);
+                        umma_f8_pair(d_tmem, ad, bd, f8p::IDESC, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit_pair_mc(&acc_full[b], 0x3);
+                    umma_commit_pair_mc(&empty[st], 0x3);
+                }
+            }
+            if (!ok) {
+                set_status(p.status, GPTQ_ERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every MMA must have finished before either CTA releases TMEM or leaves
+            umma_commit_pair_mc(drained, 0x1);
+            if (!mbar_wait(drained, 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
+        }
+        __syncwarp();
+    }
+    } else {
+        regs_grow<f8p::REGS_EPI>();
+        // ---------------- promotion (both CTAs, their own tokens) ----------------
+        const int q = warp & 3, cs = (warp - f8p::EPI_WARP0) >> 2;
+        const uint32_t t_lane = static_cast<uint32_t>(32 * q) << 16;
+        int it = 0;
+        bool stop = false;
+        for (long long t = cluster; t < p.n_tiles && !stop; t += n_clusters) {
+            int m0, n0;
+            f8_tile(p, t, f8p::PT, f8p::PT, m0, n0);
+            const int row = m0 + f8p::BM * static_cast<int>(rank) + 32 * q + lane;
+            const int col0 = n0 + f8p::EPI_COLS * cs;
+            const float* sx = p.sx + min(row, p.n_tok - 1);
+            const float* sw = p.sw + static_cast<int64_t>(min(col0, p.d_out - 1) / 128) * p.n_kb;
+            uint64_t acc[f8p::EPI_COLS / 2];
+#pragma unroll
+            for (int k = 0; k < f8p::EPI_COLS / 2; ++k) acc[k] = 0;
+            float sx_next = __ldg(sx), sw_next = __ldg(sw);
+            for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
+                const int b = it & 1;
+                const uint32_t f = __float_as_uint(sx_next * sw_next);
+                if (kb + 1 < p.n_kb) {
+                    sx_next = __ldg(sx + static_cast<int64_t>(kb + 1) * p.n_tok);
+                    sw_next = __ldg(sw + kb + 1);
+                }
+                if (!f8_warp_wait(&acc_full[b], (it >> 1) & 1, p.status, abort_flag)) {
+                    stop = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t_addr = tmem_base + t_lane +
+                                        static_cast<uint32_t>(b * f8p::PT + f8p::EPI_COLS * cs);
+                uint32_t r[2][32];
+                tmem_ld_32x32b_x32(t_addr, r[0]);
+#pragma unroll
+                for (int j = 0; j < f8p::EPI_COLS / 32; ++j) {
+                    tmem_ld_wait_for(r[j & 1]);
+                    if (j + 1 < f8p::EPI_COLS / 32) {
+                        tmem_ld_32x32b_x32(t_addr + 32 * (j + 1), r[(j + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (leader) mbar_arrive(&acc_empty[b]);
+                            else mbar_arrive_remote(mapa_shared(smem_u32(&acc_empty[b]), 0));
+                        }
+                    }
+                    f8_promote<32>(acc + 16 * j, r[j & 1], f32x2(f, f));
+                }
+            }
+            if (!stop) f8_store<T, f8p::EPI_COLS>(p, row, col0, acc);
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();     // neither CTA leaves while the pair's MMAs, copies or arrivals may touch it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, f8p::TMEM_COLS);
+}
+
+template <typename T>
+static gptq_status fp8_pair_launch(const uint8_t* X8, const uint8_t* W8, F8Params& p,
+                                   cudaStream_t s) {
+    GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_pair_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, f8p::SMEM));
+    // the warpgroups' register shares add up to what a launch with REGS per thread has
+    cudaFuncAttributes fa;
+    GPTQ_CUDA_TRY(cudaFuncGetAttributes(&fa, fp8_pair_kernel<T>));
+    if (fa.numRegs < f8p::REGS) return GPTQ_ERR_UNSUPPORTED;
+    CUtensorMap xmap, wmap;
+    GPTQ_TRY(encode_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(X8),
+                                  p.d_in, p.n_tok, p.d_in, f8p::BK, f8p::BM,
+                                  CU_TENSOR_MAP_SWIZZLE_128B));
+    GPTQ_TRY(encode_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(W8),
+                                  p.d_in, p.d_out, p.d_in, f8p::BK, f8p::BNC,
+                                  CU_TENSOR_MAP_SWIZZLE_128B));
+    p.n_mt = (p.n_tok - 1) / f8p::PT + 1;
+    p.n_nt = (p.d_out - 1) / f8p::PT + 1;
+    p.n_tiles = static_cast<long long>(p.n_mt) * p.n_nt;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr;
+    cfg.blockDim = dim3(f8p::THREADS);
+    cfg.dynamicSmemBytes = f8p::SMEM;
+    cfg.stream = s;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(p.n_tiles, num_sms() / 2)));
+    GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T>, xmap, wmap, p));
+    GPTQ_LAUNCHED();
+    return GPTQ_OK;
+}
+
+template <typename T>
+static gptq_status fp8_linear_launch(const uint8_t* X8, const uint8_t* W8, F8Params& p,
+                                     cudaStream_t s) {
+    p.vec_ok = p.d_out % Vec<T>::N == 0;
+    const long long pair_tiles = static_cast<long long>((p.n_tok - 1) / f8p::PT + 1) *
+                                 ((p.d_out - 1) / f8p::PT + 1);
+    if (p.n_tok > 128 && 2 * pair_tiles >= num_sms()) return fp8_pair_launch<T>(X8, W8, p, s);
+    return fp8_gemm_launch<T>(X8, W8, p, s);
 }
 
 }  // namespace gq
@@ -299,8 +564,8 @@ extern "C" gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int6
     p.status = status_dev;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (y_dtype) {
-        case GPTQ_DTYPE_F16: return gq::fp8_gemm_launch<__half>(X8, W8, p, s);
-        case GPTQ_DTYPE_BF16: return gq::fp8_gemm_launch<__nv_bfloat16>(X8, W8, p, s);
-        default: return gq::fp8_gemm_launch<float>(X8, W8, p, s);
+        case GPTQ_DTYPE_F16: return gq::fp8_linear_launch<__half>(X8, W8, p, s);
+        case GPTQ_DTYPE_BF16: return gq::fp8_linear_launch<__nv_bfloat16>(X8, W8, p, s);
+        default: return gq::fp8_linear_launch<float>(X8, W8, p, s);
     }
 }
