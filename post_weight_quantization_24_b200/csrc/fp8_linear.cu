@@ -37,7 +37,7 @@ static_assert(SMEM <= 227 * 1024, "shared memory");
 struct F8Params {
     int n_tok, d_in, d_out;
     int n_mt, n_nt, n_kb;
-    long long n_tiles;
+    int n_tiles;
     const float* sx;      // [n_kb x n_tok]
     const float* sw;      // [ceil(d_out/128) x n_kb]
     const void* R;
@@ -48,11 +48,11 @@ struct F8Params {
 
 // Tiles run in bands of 8 token tiles with the token tile varying fastest, so the CTAs that run
 // together share weight tiles and activation rows in L2.
-__device__ __forceinline__ void f8_tile(const F8Params& p, long long t, int bm, int bn, int& m0,
+__device__ __forceinline__ void f8_tile(const F8Params& p, int t, int bm, int bn, int& m0,
                                         int& n0) {
-    const long long per_band = static_cast<long long>(f8::BAND) * p.n_nt;
-    const int band = static_cast<int>(t / per_band);
-    const int rem = static_cast<int>(t - band * per_band);
+    const int per_band = f8::BAND * p.n_nt;
+    const int band = t / per_band;
+    const int rem = t - band * per_band;
     const int band_m = min(f8::BAND, p.n_mt - band * f8::BAND);
     m0 = (band * f8::BAND + rem % band_m) * bm;
     n0 = (rem / band_m) * bn;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
-            for (long long t = blockIdx.x; t < p.n_tiles && !*abort_flag; t += gridDim.x) {
+            for (int t = blockIdx.x; t < p.n_tiles && !*abort_flag; t += gridDim.x) {
                 int m0, n0;
                 f8_tile(p, t, f8::BM, f8::BN, m0, n0);
                 for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (long long t = blockIdx.x; ok && t < p.n_tiles && !*abort_flag; t += gridDim.x) {
+            for (int t = blockIdx.x; ok && t < p.n_tiles && !*abort_flag; t += gridDim.x) {
                 for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
                     const int st = it % f8::STAGES, b = it % f8::ACCS;
                     if (!mbar_wait(&acc_empty[b], ((it / f8::ACCS) & 1) ^ 1) ||
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
         const uint32_t t_lane = static_cast<uint32_t>(32 * q) << 16;
         int it = 0;
         bool stop = false;
-        for (long long t = blockIdx.x; t < p.n_tiles && !stop; t += gridDim.x) {
+        for (int t = blockIdx.x; t < p.n_tiles && !stop; t += gridDim.x) {
             int m0, n0;
             f8_tile(p, t, f8::BM, f8::BN, m0, n0);
             const int row = m0 + 32 * q + lane;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
                 for (int j = 1; j < f8::EPI_COLS / 32; ++j) tmem_ld_use(r[j]);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[b]);
+                if (lane == 0) mbar_arrive_relaxed(&acc_empty[b]);
 #pragma unroll
                 for (int j = 0; j < f8::EPI_COLS / 32; ++j) f8_promote<32>(acc + 16 * j, r[j], f32x2(f, f));
             }
@@ -262,6 +262,14 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, f8::TMEM_COLS);
+}
+
+static gptq_status f8_tiles(F8Params& p) {
+    // tile numbers (with a launch's stride added) stay within 31 bits
+    const long long n = static_cast<long long>(p.n_mt) * p.n_nt;
+    if (n > 0x7FFF0000 || f8::BAND * static_cast<long long>(p.n_nt) > 0x7FFF0000) return GPTQ_ERR_ARG;
+    p.n_tiles = static_cast<int>(n);
+    return GPTQ_OK;
 }
 
 template <typename T>
@@ -278,8 +286,8 @@ static gptq_status fp8_gemm_launch(const uint8_t* X8, const uint8_t* W8, F8Param
                                   CU_TENSOR_MAP_SWIZZLE_128B));
     p.n_mt = (p.n_tok - 1) / f8::BM + 1;
     p.n_nt = (p.d_out - 1) / f8::BN + 1;
-    p.n_tiles = static_cast<long long>(p.n_mt) * p.n_nt;
-    const int grid = static_cast<int>(std::min<long long>(p.n_tiles, num_sms()));
+    GPTQ_TRY(f8_tiles(p));
+    const int grid = std::min(p.n_tiles, num_sms());
     fp8_gemm_kernel<T><<<grid, f8::THREADS, f8::SMEM, s>>>(xmap, wmap, p);
     GPTQ_LAUNCHED();
     return GPTQ_OK;
@@ -287,48 +295,124 @@ static gptq_status fp8_gemm_launch(const uint8_t* X8, const uint8_t* W8, F8Param
 
 // ---------------------------------------------------------------------------------------
 // Pair kernel for large calls: two CTAs of a cluster share one 256 x 256 tile (tcgen05
-// cta_group::2, M256 N256 K32). Each CTA loads its 128 tokens and its 128 of the tile's 256
-// channels per block, 32 KB for 8.4 M products instead of the 64 KB that four 128 x 128 tiles
-// need, and promotes its own 128 tokens x 256 channels. Synchronisation as in the Hessian's pair
-// kernel: both CTAs' bytes complete on the leader's stage barrier, the leader's commits arrive on
-// both CTAs' barriers, both CTAs' promotion warps release an accumulator on the leader's.
+// cta_group::2). Each CTA loads its 128 tokens and half of the tile's channels per block, 32 KB
+// for 8.4 M products instead of the 64 KB that four 128 x 128 tiles need, and promotes its own 128
+// tokens x 256 channels. Synchronisation as in the Hessian's pair kernel: both CTAs' bytes
+// complete on the leader's stage barrier, the leader's commits arrive on both CTAs' barriers, both
+// CTAs' promotion warps release an accumulator on the leader's.
+//
+// Two issuer warps take the blocks in turn, each with its own 256-column accumulator: a thread
+// that commits and then waits on a barrier loses about 45 + 50 cycles per commit and wait, because
+// nothing of its next block is queued meanwhile. One issuer took 648 cycles per block, two take
+// the tensor pipe's 512 (measured on synthetic blocks; splitting N instead of the blocks took
+// 692). Each of the two promotion warpgroups owns half of the columns.
 // ---------------------------------------------------------------------------------------
 namespace f8p {
 constexpr int PT = 256;                              // pair tile edge
 constexpr int BM = 128, BNC = 128;                   // tokens, channels loaded per CTA
-constexpr int BK = 128, STAGES = 6;
+constexpr int BK = 128, STAGES = 4;
 constexpr int A_BYTES = BM * BK, STAGE = A_BYTES + BNC * BK;
-// Warpgroup 0 holds the producer and the issuer, warpgroups 1 and 2 promote: a thread keeps one
-// token's 128 sums and two 32-column loads in flight, more than an even share of registers.
-constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, EPI_COLS = 128;
-constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+constexpr int HN = 128;                              // columns of a promotion warpgroup
+// Warpgroup 0 holds the producer and the two issuers, warpgroups 1 and 2 promote: a
+// thread keeps one token's 128 sums and two 32-column loads in flight, more than an even share
+// of registers.
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
+constexpr int EPI_THREADS = EPI_WARPS * 32;
+constexpr int THREADS = EPI_WARP0 * 32 + EPI_THREADS;
 constexpr int REGS = 168, REGS_IO = 56, REGS_EPI = 224;
 static_assert(REGS_IO * 128 + REGS_EPI * 256 <= REGS * THREADS, "register shares");
-constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+// A warp's rows leave through shared memory: boxes of 32 rows x 128 bytes (128-byte swizzle), two at
+// a time, written by TMA while the next tile is computed.
+constexpr int BOX_BYTES = 32 * 128;
+constexpr int STAGING = EPI_WARPS * 2 * BOX_BYTES;
+constexpr int SMEM = 1024 + STAGES * STAGE + STAGING + 256;
 constexpr uint32_t TMEM_COLS = 512;                  // two accumulators of 256 columns
 constexpr uint32_t IDESC = umma_idesc_e4m3(PT, PT);
-static_assert(SMEM <= 227 * 1024, "shared memory");
+static_assert(SMEM <= 227 * 1024 && STAGES % 2 == 0, "shared memory; stages in turn");
 }  // namespace f8p
+
+// Two boxes of R, 32 rows x (128 bytes of columns) each, from column `col`.
+template <typename T>
+__device__ __forceinline__ void f8_load_residual(const CUtensorMap* rmap, uint8_t* buf, uint64_t* bar,
+                                                 int col, int row0) {
+    constexpr int COLS = 32 * Vec<T>::N / 4;         // 128 bytes: 64 columns, or 32 of fp32
+    mbar_arrive_expect_tx(bar, 2 * f8p::BOX_BYTES);
+    tma_load_2d(buf, rmap, bar, col, row0);
+    tma_load_2d(buf + f8p::BOX_BYTES, rmap, bar, col + COLS, row0);
+}
+
+// One warp's 32 rows x 128 columns -> Y (+ R) through `buf` (two boxes). With R, its first two
+// boxes are on their way to buf already (f8_load_residual on `bar`, whose phase is r_phase).
+// Boxes and rows past Y's edges are dropped by TMA. False if a wait gave up.
+template <typename T>
+__device__ __forceinline__ bool f8_store_boxes(const CUtensorMap* ymap, const CUtensorMap* rmap,
+                                               bool res, int n_tok, int d_out, int row0, int col0,
+                                               const uint64_t (&acc)[f8p::HN / 2], uint8_t* buf,
+                                               uint64_t* bar, uint32_t& r_phase, int* status,
+                                               volatile int* abort_flag) {
+    constexpr int N = Vec<T>::N, COLS = 8 * N, ROUND = 2 * COLS;
+    const int lane = lane_id();
+#pragma unroll
+    for (int c0 = 0; c0 < f8p::HN; c0 += ROUND) {
+        if (c0 > 0) {                                // fp32: the second round reuses the boxes
+            if (lane == 0) {
+                bulk_wait_read<0>();
+                if (res) f8_load_residual<T>(rmap, buf, bar, col0 + c0, row0);
+            }
+            __syncwarp();
+        }
+        if (res) {
+            if (!f8_warp_wait(bar, r_phase, status, abort_flag)) return false;
+            r_phase ^= 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {               // 16-byte pieces of the row
+            uint8_t* at = buf + (i >> 3) * f8p::BOX_BYTES + lane * 128 + (((i & 7) ^ (lane & 7)) << 4);
+            float v[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = f32x2_get(acc[(c0 + i * N + e) / 2], e & 1);
+            if (res) {
+                float f[N];
+                Vec<T>::unpack(*reinterpret_cast<const uint4*>(at), f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] += f[e];
+            }
+            *reinterpret_cast<uint4*>(at) = Vec<T>::pack(v);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < n_tok) {             // whole boxes past the edge are not issued
+            if (col0 + c0 < d_out) tma_store_2d(ymap, buf, col0 + c0, row0);
+            if (col0 + c0 + COLS < d_out)
+                tma_store_2d(ymap, buf + f8p::BOX_BYTES, col0 + c0 + COLS, row0);
+            bulk_commit();
+        }
+    }
+    return true;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(f8p::THREADS, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                    const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap rmap,
                     const F8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + f8p::STAGES * f8p::STAGE);
-    uint64_t* empty = full + f8p::STAGES;
-    uint64_t* acc_full = empty + f8p::STAGES;
-    uint64_t* acc_empty = acc_full + 2;
-    uint64_t* drained = acc_empty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    uint8_t* staging = smem + f8p::STAGES * f8p::STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + f8p::STAGING);   // [STAGES] leader
+    uint64_t* empty = full + f8p::STAGES;            // [STAGES] each CTA
+    uint64_t* acc_full = empty + f8p::STAGES;        // [2] each CTA
+    uint64_t* acc_empty = acc_full + 2;              // [2] leader: both CTAs have read it
+    uint64_t* drained = acc_empty + 2;               // [2] leader, one per issuer
+    uint64_t* r_full = drained + 2;                  // [EPI_WARPS] each CTA: a warp's part of R
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(r_full + f8p::EPI_WARPS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = warp_id(), lane = lane_id();
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    const long long cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+    const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < f8p::STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -337,8 +421,9 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 2 * f8p::EPI_WARPS);
+            mbar_init(&drained[b], 1);
         }
-        mbar_init(drained, 1);
+        for (int w = 0; w < f8p::EPI_WARPS; ++w) mbar_init(&r_full[w], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
@@ -355,12 +440,11 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
 
     if (warp < f8p::EPI_WARP0) {
-    regs_shrink<f8p::REGS_IO>();
-    if (warp == 0) {
-        // ---------------- TMA producer (both CTAs) ----------------
-        if (lane == 0) {
+        regs_shrink<f8p::REGS_IO>();
+        if (warp == 0 && lane == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
             int it = 0;
-            for (long long t = cluster; t < p.n_tiles && !*abort_flag; t += n_clusters) {
+            for (int t = cluster; t < p.n_tiles && !*abort_flag; t += n_clusters) {
                 int m0, n0;
                 f8_tile(p, t, f8p::PT, f8p::PT, m0, n0);
                 m0 += f8p::BM * static_cast<int>(rank);
@@ -390,32 +474,35 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
                     }
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (leader) ----------------
-        if (leader && lane == 0) {
-            int it = 0;
+        } else if ((warp == 1 || warp == 2) && leader && lane == 0) {
+            // ---------------- MMA issuers (leader), every other block each ----------------
+            const int b = warp - 1;
+            const int per_tile = p.n_kb;
+            const int mine = cluster < p.n_tiles ? (p.n_tiles - 1 - cluster) / n_clusters + 1 : 0;
+            const long long blocks = static_cast<long long>(mine) * per_tile;
             bool ok = true;
-            for (long long t = cluster; ok && t < p.n_tiles && !*abort_flag; t += n_clusters) {
-                for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
-                    const int st = it % f8p::STAGES, b = it & 1;
-                    if (!mbar_wait(&full[st], (it / f8p::STAGES) & 1) ||
-                        !mbar_wait(&acc_empty[b], ((it >> 1) & 1) ^ 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * f8p::PT);
-                    const uint32_t s0 = smem_u32(smem + st * f8p::STAGE);
+            int st = b;
+            uint32_t st_phase = 0, acc_phase = 1;
+            for (long long it = b; it < blocks && !*abort_flag; it += 2) {
+                if (!mbar_wait(&full[st], st_phase) || !mbar_wait(&acc_empty[b], acc_phase)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * f8p::PT);
+                const uint32_t s0 = smem_u32(smem + st * f8p::STAGE);
 #pragma unroll
-                    for (int kk = 0; kk < f8p::BK / 32; ++kk) {
-                        const uint64_t ad = umma_desc_sw128(s0 + kk * 32, 16, 1024);
-                        const uint64_t bd = umma_desc_sw128(s0 + f8p::A_BYTES + kk * 32, 16, 1024);
-                        umma_f8_pair(d_tmem, ad, bd, f8p::IDESC, kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit_pair_mc(&acc_full[b], 0x3);
-                    umma_commit_pair_mc(&empty[st], 0x3);
+                for (int kk = 0; kk < f8p::BK / 32; ++kk)
+                    umma_f8_pair(d_tmem, umma_desc_sw128(s0 + kk * 32, 16, 1024),
+                                 umma_desc_sw128(s0 + f8p::A_BYTES + kk * 32, 16, 1024), f8p::IDESC,
+                                 kk > 0 ? 1u : 0u);
+                umma_commit_pair_mc(&acc_full[b], 0x3);
+                umma_commit_pair_mc(&empty[st], 0x3);
+                acc_phase ^= 1;
+                st += 2;
+                if (st >= f8p::STAGES) {       // STAGES is even: both issuers keep their parity
+                    st -= f8p::STAGES;
+                    st_phase ^= 1;
                 }
             }
             if (!ok) {
@@ -423,34 +510,44 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
                 *abort_flag = 1;
             }
             // every MMA must have finished before either CTA releases TMEM or leaves
-            umma_commit_pair_mc(drained, 0x1);
-            if (!mbar_wait(drained, 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
+            umma_commit_pair_mc(&drained[b], 0x1);
+            if (!mbar_wait(&drained[b], 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
         }
         __syncwarp();
-    }
     } else {
-        regs_grow<f8p::REGS_EPI>();
         // ---------------- promotion (both CTAs, their own tokens) ----------------
-        const int q = warp & 3, cs = (warp - f8p::EPI_WARP0) >> 2;
-        const uint32_t t_lane = static_cast<uint32_t>(32 * q) << 16;
+        regs_grow<f8p::REGS_EPI>();
+        const int q = warp & 3, h = (warp - f8p::EPI_WARP0) >> 2;
+        const int row_in = f8p::BM * static_cast<int>(rank) + 32 * q;
+        const uint32_t t_half = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                static_cast<uint32_t>(h * f8p::HN);
+        const int ew = warp - f8p::EPI_WARP0;
+        uint8_t* buf = staging + ew * 2 * f8p::BOX_BYTES;
+        uint64_t* r_bar = &r_full[ew];
+        uint32_t r_phase = 0;
+        const bool boxes = p.vec_ok != 0, res = p.R != nullptr;
         int it = 0;
         bool stop = false;
-        for (long long t = cluster; t < p.n_tiles && !stop; t += n_clusters) {
+        for (int t = cluster; t < p.n_tiles && !stop; t += n_clusters) {
             int m0, n0;
             f8_tile(p, t, f8p::PT, f8p::PT, m0, n0);
-            const int row = m0 + f8p::BM * static_cast<int>(rank) + 32 * q + lane;
-            const int col0 = n0 + f8p::EPI_COLS * cs;
-            const float* sx = p.sx + min(row, p.n_tok - 1);
-            const float* sw = p.sw + static_cast<int64_t>(min(col0, p.d_out - 1) / 128) * p.n_kb;
-            uint64_t acc[f8p::EPI_COLS / 2];
+            const int col0 = n0 + f8p::HN * h;
+            if (boxes && res && lane == 0) {
+                bulk_wait_read<0>();                 // the last tile has left the boxes
+                f8_load_residual<T>(&rmap, buf, r_bar, col0, m0 + row_in);
+            }
+            uint64_t acc[f8p::HN / 2];
 #pragma unroll
-            for (int k = 0; k < f8p::EPI_COLS / 2; ++k) acc[k] = 0;
+            for (int k = 0; k < f8p::HN / 2; ++k) acc[k] = 0;
+            const float* sx = p.sx + min(m0 + row_in + lane, p.n_tok - 1);
+            const float* sw = p.sw + static_cast<int64_t>(min(col0, p.d_out - 1) / 128) * p.n_kb;
             float sx_next = __ldg(sx), sw_next = __ldg(sw);
             for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
                 const int b = it & 1;
                 const uint32_t f = __float_as_uint(sx_next * sw_next);
                 if (kb + 1 < p.n_kb) {
-                    sx_next = __ldg(sx + static_cast<int64_t>(kb + 1) * p.n_tok);
+                    sx += p.n_tok;
+                    sx_next = __ldg(sx);
                     sw_next = __ldg(sw + kb + 1);
                 }
                 if (!f8_warp_wait(&acc_full[b], (it >> 1) & 1, p.status, abort_flag)) {
@@ -458,28 +555,44 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t t_addr = tmem_base + t_lane +
-                                        static_cast<uint32_t>(b * f8p::PT + f8p::EPI_COLS * cs);
+                const uint32_t t_addr = t_half + static_cast<uint32_t>(b * f8p::PT);
+                // 128 columns in four loads; the accumulator is handed back as soon as the last
+                // has arrived, before the last two are added
                 uint32_t r[2][32];
                 tmem_ld_32x32b_x32(t_addr, r[0]);
-#pragma unroll
-                for (int j = 0; j < f8p::EPI_COLS / 32; ++j) {
-                    tmem_ld_wait_for(r[j & 1]);
-                    if (j + 1 < f8p::EPI_COLS / 32) {
-                        tmem_ld_32x32b_x32(t_addr + 32 * (j + 1), r[(j + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (leader) mbar_arrive(&acc_empty[b]);
-                            else mbar_arrive_remote(mapa_shared(smem_u32(&acc_empty[b]), 0));
-                        }
-                    }
-                    f8_promote<32>(acc + 16 * j, r[j & 1], f32x2(f, f));
+                tmem_ld_32x32b_x32(t_addr + 32, r[1]);
+                tmem_ld_wait_for(r[0]);
+                tmem_ld_use(r[1]);
+                f8_promote<32>(acc, r[0], f32x2(f, f));
+                tmem_ld_32x32b_x32(t_addr + 64, r[0]);
+                f8_promote<32>(acc + 16, r[1], f32x2(f, f));
+                tmem_ld_32x32b_x32(t_addr + 96, r[1]);
+                tmem_ld_wait_for(r[0]);
+                tmem_ld_use(r[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive_relaxed(&acc_empty[b]);
+                    else mbar_arrive_relaxed_cluster(mapa_shared(smem_u32(&acc_empty[b]), 0));
                 }
+                f8_promote<32>(acc + 32, r[0], f32x2(f, f));
+                f8_promote<32>(acc + 48, r[1], f32x2(f, f));
             }
-            if (!stop) f8_store<T, f8p::EPI_COLS>(p, row, col0, acc);
+            if (stop) break;
+            if (boxes) {
+                if (!res) {
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+                }
+                stop = !f8_store_boxes<T>(&ymap, &rmap, res, p.n_tok, p.d_out, m0 + row_in, col0, acc,
+                                          buf, r_bar, r_phase, p.status, abort_flag);
+            } else {
+                f8_store<T, f8p::HN>(p, m0 + row_in + lane, col0, acc);
+            }
         }
+        // a residual that was asked for and not used (after a timeout) must have landed
+        if (boxes && res && stop && lane == 0) mbar_wait(r_bar, r_phase);
+        if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
 
@@ -489,6 +602,21 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem_base, f8p::TMEM_COLS);
 }
+
+template <typename T>
+struct F8MapType;
+template <>
+struct F8MapType<__half> {
+    static constexpr CUtensorMapDataType value = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+};
+template <>
+struct F8MapType<__nv_bfloat16> {
+    static constexpr CUtensorMapDataType value = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+};
+template <>
+struct F8MapType<float> {
+    static constexpr CUtensorMapDataType value = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+};
 
 template <typename T>
 static gptq_status fp8_pair_launch(const uint8_t* X8, const uint8_t* W8, F8Params& p,
@@ -506,9 +634,19 @@ static gptq_status fp8_pair_launch(const uint8_t* X8, const uint8_t* W8, F8Param
     GPTQ_TRY(encode_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(W8),
                                   p.d_in, p.d_out, p.d_in, f8p::BK, f8p::BNC,
                                   CU_TENSOR_MAP_SWIZZLE_128B));
+    CUtensorMap ymap{}, rmap{};
+    if (p.vec_ok) {
+        const uint64_t row = static_cast<uint64_t>(p.d_out) * sizeof(T);
+        GPTQ_TRY(encode_tensor_map_2d(&ymap, F8MapType<T>::value, p.Y, p.d_out, p.n_tok, row,
+                                      128 / sizeof(T), 32, CU_TENSOR_MAP_SWIZZLE_128B));
+        if (p.R)
+            GPTQ_TRY(encode_tensor_map_2d(&rmap, F8MapType<T>::value, const_cast<void*>(p.R), p.d_out,
+                                          p.n_tok, row, 128 / sizeof(T), 32,
+                                          CU_TENSOR_MAP_SWIZZLE_128B));
+    }
     p.n_mt = (p.n_tok - 1) / f8p::PT + 1;
     p.n_nt = (p.d_out - 1) / f8p::PT + 1;
-    p.n_tiles = static_cast<long long>(p.n_mt) * p.n_nt;
+    GPTQ_TRY(f8_tiles(p));
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr;
     cfg.blockDim = dim3(f8p::THREADS);
@@ -520,8 +658,8 @@ static gptq_status fp8_pair_launch(const uint8_t* X8, const uint8_t* W8, F8Param
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(p.n_tiles, num_sms() / 2)));
-    GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T>, xmap, wmap, p));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.n_tiles, num_sms() / 2)));
+    GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T>, xmap, wmap, ymap, rmap, p));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }
