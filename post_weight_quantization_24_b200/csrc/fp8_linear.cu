@@ -6,33 +6,20 @@
 // (4 x tcgen05.mma kind::f8f6f4 of K = 32, fp32 accumulator in TMEM) and the sum over blocks
 // is kept in registers: acc = fma(partial, sx*sw, acc), rounded to nearest.
 //
-// Persistent kernel, one CTA per SM, tiles of 128 tokens x 128 channels, ring of 6 stages:
-//   warp 0     TMA producer: per block the 128 x 128-byte tiles of X and W (128-byte swizzle);
-//   warp 1     TMEM allocator and MMA issuer, into one of four 128-column accumulators;
-//   warps 2-9  promotion: a thread owns one token row and 64 columns.
-// Tokens and channels past the edges are zero-filled by TMA and not stored.
-// Every mbarrier wait is bounded; on timeout the kernel records GPTQ_ERR_TIMEOUT, drains its
-// copies and MMAs, frees TMEM and returns.
+// Two kernels, both fed by TMA (128-byte swizzle) with bounded waits everywhere: on timeout a
+// kernel records GPTQ_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns. Tokens and
+// channels past the edges are zero-filled by TMA and not stored.
+//   fp8_pair_kernel    256 tokens x 256 channels per CTA pair, for calls with enough such tiles to
+//                      fill the GPU: bound by the tensor cores and, over long runs, by power;
+//   fp8_stream_kernel  128 channels x 16 to 128 tokens per CTA, the input channels split over a
+//                      cluster: for all other calls, bound by streaming the weights.
 #include <algorithm>
+#include <atomic>
 
 #include "internal.cuh"
 #include "vec.cuh"
 
 namespace gq {
-
-namespace f8 {
-constexpr int BM = 128, BN = 128, BK = 128, STAGES = 6;
-constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
-constexpr int STAGE = A_BYTES + B_BYTES;
-constexpr int ACCS = 4;                              // TMEM accumulators of BN columns
-constexpr uint32_t TMEM_COLS = ACCS * BN;
-constexpr int EPI_WARPS = 8, EPI_COLS = 64;          // 4 lane quarters x 2 column halves
-constexpr int THREADS = (2 + EPI_WARPS) * 32;
-constexpr int SMEM = 1024 + STAGES * STAGE + 256;
-constexpr int BAND = 8;
-constexpr uint32_t IDESC = umma_idesc_e4m3(BM, BN);
-static_assert(SMEM <= 227 * 1024, "shared memory");
-}  // namespace f8
 
 struct F8Params {
     int n_tok, d_in, d_out;
@@ -45,18 +32,6 @@ struct F8Params {
     int vec_ok;           // rows of Y and R start on 16-byte boundaries
     int* status;
 };
-
-// Tiles run in bands of 8 token tiles with the token tile varying fastest, so the CTAs that run
-// together share weight tiles and activation rows in L2.
-__device__ __forceinline__ void f8_tile(const F8Params& p, int t, int bm, int bn, int& m0,
-                                        int& n0) {
-    const int per_band = f8::BAND * p.n_nt;
-    const int band = t / per_band;
-    const int rem = t - band * per_band;
-    const int band_m = min(f8::BAND, p.n_mt - band * f8::BAND);
-    m0 = (band * f8::BAND + rem % band_m) * bm;
-    n0 = (rem / band_m) * bn;
-}
 
 // NC accumulated columns of one row -> Y (+ R), columns col0 .. min(col0 + NC, d_out)
 template <typename T, int NC>
@@ -110,187 +85,251 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, int
     return false;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(f8::THREADS, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                    const F8Params p) {
+// ---------------------------------------------------------------------------------------
+// Streaming kernel: Y^T tiles of 128 channels x NT tokens, the weights as the MMA's M operand, so
+// that a few tokens cost a narrow N instead of an M of 128 rows. A cluster of S CTAs splits the
+// tile's input channels; each CTA streams its part of the weights (16 KB per block through a
+// ring of stages), and the S partial sums are added over distributed shared memory in rank order,
+// so equal inputs give equal bits. One CTA's ring keeps about 100 KB in flight, and two fit an SM.
+//   warp 0    TMA producer            warps 1, 2  MMA issuers, every other block each
+//   warps 3-  promotion: a thread owns one channel and EC tokens. The factors sx*sw (one per token
+//             and block) are put into shared memory for FBLK blocks at a time, which exposes
+//             their latency once instead of once per block.
+// ---------------------------------------------------------------------------------------
+namespace f8s {
+constexpr int BM = 128, BK = 128;
+template <int NT>
+struct Cfg {
+    static constexpr int PER_SM = NT == 128 ? 1 : 2;              // CTAs that fit an SM
+    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 6;
+    static constexpr int A_BYTES = BM * BK, STAGE = A_BYTES + NT * BK;
+    static constexpr int ACCS = NT == 128 ? 2 : 4;
+    static constexpr uint32_t TMEM_COLS = ACCS * NT;
+    static constexpr int EC = NT <= 32 ? 16 : 32, EPI_WARPS = 4 * (NT / EC);
+    static constexpr int EPI_THREADS = EPI_WARPS * 32, THREADS = 96 + EPI_THREADS;
+    static constexpr int FBLK = NT == 128 ? 16 : 32;             // blocks of factors kept
+    static constexpr int SMEM = 1024 + STAGES * STAGE + FBLK * NT * 4 + 256;
+    static constexpr uint32_t IDESC = umma_idesc_e4m3(BM, NT);
+    static_assert(NT * BM * 4 <= STAGES * STAGE, "the partial sums reuse the ring");
+    static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024, "CTAs per SM");
+};
+}  // namespace f8s
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr));
+    return v;
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
+    fp8_stream_kernel(const __grid_constant__ CUtensorMap xmap,
+                      const __grid_constant__ CUtensorMap wmap, const F8Params p, int splits) {
+    using C = f8s::Cfg<NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + f8::STAGES * f8::STAGE);
-    uint64_t* empty = full + f8::STAGES;
-    uint64_t* acc_full = empty + f8::STAGES;
-    uint64_t* acc_empty = acc_full + f8::ACCS;
-    uint64_t* drained = acc_empty + f8::ACCS;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    float* factors = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);      // [FBLK][NT]
+    uint64_t* full = reinterpret_cast<uint64_t*>(factors + C::FBLK * NT);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* acc_full = empty + C::STAGES;
+    uint64_t* acc_empty = acc_full + C::ACCS;
+    uint64_t* drained = acc_empty + C::ACCS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = warp_id(), lane = lane_id();
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int tile = static_cast<int>(blockIdx.x) / splits;
+    const int t0 = (tile % p.n_mt) * NT, c0 = (tile / p.n_mt) * f8s::BM;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.n_kb) * rank / splits);
+    const int n_kb = static_cast<int>(static_cast<int64_t>(p.n_kb) * (rank + 1) / splits) - kb0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < f8::STAGES; ++s) {
+        for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < f8::ACCS; ++b) {
+        for (int b = 0; b < C::ACCS; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], f8::EPI_WARPS);
+            mbar_init(&acc_empty[b], C::EPI_WARPS);
         }
-        mbar_init(drained, 1);
+        mbar_init(&drained[0], 1);
+        mbar_init(&drained[1], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
         tma_prefetch_desc(&wmap);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, f8::TMEM_COLS);
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();         // nothing the previous kernel may have written was read so far
 
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
-            for (int t = blockIdx.x; t < p.n_tiles && !*abort_flag; t += gridDim.x) {
-                int m0, n0;
-                f8_tile(p, t, f8::BM, f8::BN, m0, n0);
-                for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
-                    const int st = it % f8::STAGES;
-                    if (!mbar_wait(&empty[st], ((it / f8::STAGES) & 1) ^ 1)) {
-                        set_status(p.status, GPTQ_ERR_TIMEOUT);
-                        *abort_flag = 1;
-                        break;
-                    }
-                    uint8_t* sa = smem + st * f8::STAGE;
-                    mbar_arrive_expect_tx(&full[st], f8::STAGE);
-                    tma_load_2d(sa, &xmap, &full[st], kb * f8::BK, m0);
-                    tma_load_2d(sa + f8::A_BYTES, &wmap, &full[st], kb * f8::BK, n0);
+            for (; it < n_kb && !*abort_flag; ++it) {
+                const int st = it % C::STAGES;
+                if (!mbar_wait(&empty[st], ((it / C::STAGES) & 1) ^ 1)) {
+                    set_status(p.status, GPTQ_ERR_TIMEOUT);
+                    *abort_flag = 1;
+                    break;
                 }
+                uint8_t* sa = smem + st * C::STAGE;
+                const int x = (kb0 + it) * f8s::BK;
+                mbar_arrive_expect_tx(&full[st], C::STAGE);
+                tma_load_2d(sa, &wmap, &full[st], x, c0);
+                tma_load_2d(sa + C::A_BYTES, &xmap, &full[st], x, t0);
             }
-            const int n_tail = it < f8::STAGES ? it : f8::STAGES;
+            const int n_tail = it < C::STAGES ? it : C::STAGES;
             for (int k = it - n_tail; k < it; ++k) {
-                if (!mbar_wait(&full[k % f8::STAGES], (k / f8::STAGES) & 1)) {
+                if (!mbar_wait(&full[k % C::STAGES], (k / C::STAGES) & 1)) {
                     set_status(p.status, GPTQ_ERR_TIMEOUT);
                     *abort_flag = 1;
                 }
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp < 3) {
         if (lane == 0) {
-            int it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < p.n_tiles && !*abort_flag; t += gridDim.x) {
-                for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
-                    const int st = it % f8::STAGES, b = it % f8::ACCS;
-                    if (!mbar_wait(&acc_empty[b], ((it / f8::ACCS) & 1) ^ 1) ||
-                        !mbar_wait(&full[st], (it / f8::STAGES) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * f8::BN);
-                    const uint32_t s0 = smem_u32(smem + st * f8::STAGE);
-#pragma unroll
-                    for (int kk = 0; kk < f8::BK / 32; ++kk) {
-                        // K-major rows of 128 B; a k-step of 32 codes is 32 B along the row
-                        const uint64_t ad = umma_desc_sw128(s0 + kk * 32, 16, 1024);
-                        const uint64_t bd = umma_desc_sw128(s0 + f8::A_BYTES + kk * 32, 16, 1024);
-                        umma_f8(d_tmem, ad, bd, f8::IDESC, kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit(&empty[st]);
-                    umma_commit(&acc_full[b]);
+            for (int it = warp - 1; it < n_kb && !*abort_flag; it += 2) {
+                const int st = it % C::STAGES, b = it % C::ACCS;
+                if (!mbar_wait(&acc_empty[b], ((it / C::ACCS) & 1) ^ 1) ||
+                    !mbar_wait(&full[st], (it / C::STAGES) & 1)) {
+                    ok = false;
+                    break;
                 }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * NT);
+                const uint32_t s0 = smem_u32(smem + st * C::STAGE);
+#pragma unroll
+                for (int kk = 0; kk < f8s::BK / 32; ++kk) {
+                    // K-major rows of 128 B; a k-step of 32 codes is 32 B along the row
+                    umma_f8(d_tmem, umma_desc_sw128(s0 + kk * 32, 16, 1024),
+                            umma_desc_sw128(s0 + C::A_BYTES + kk * 32, 16, 1024), C::IDESC,
+                            kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&acc_full[b]);
+                umma_commit(&empty[st]);
             }
             if (!ok) {
                 set_status(p.status, GPTQ_ERR_TIMEOUT);
                 *abort_flag = 1;
             }
-            umma_commit(drained);
-            if (!mbar_wait(drained, 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
+            umma_commit(&drained[warp - 1]);
+            if (!mbar_wait(&drained[warp - 1], 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
         }
         __syncwarp();
     } else {
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        const uint32_t t_lane = static_cast<uint32_t>(32 * q) << 16;
-        int it = 0;
-        bool stop = false;
-        for (int t = blockIdx.x; t < p.n_tiles && !stop; t += gridDim.x) {
-            int m0, n0;
-            f8_tile(p, t, f8::BM, f8::BN, m0, n0);
-            const int row = m0 + 32 * q + lane;
-            const float* sx = p.sx + min(row, p.n_tok - 1);
-            const float* sw = p.sw + static_cast<int64_t>(n0 / 128) * p.n_kb;
-            uint64_t acc[f8::EPI_COLS / 2];
+        const int q = warp & 3, g = (warp - 3) >> 2;       // channel quarter, token group
+        const int e = threadIdx.x - 96;                    // promotion thread
+        const uint32_t t_addr0 = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                 static_cast<uint32_t>(g * C::EC);
+        const float* sx = p.sx + static_cast<int64_t>(kb0) * p.n_tok + t0;
+        const float* sw = p.sw + static_cast<int64_t>(c0 / 128) * p.n_kb + kb0;
+        float acc[C::EC];
 #pragma unroll
-            for (int k = 0; k < f8::EPI_COLS / 2; ++k) acc[k] = 0;
-            float sx_next = __ldg(sx), sw_next = __ldg(sw);
-            for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
-                const int b = it % f8::ACCS;
-                const uint32_t f = __float_as_uint(sx_next * sw_next);
-                if (kb + 1 < p.n_kb) {
-                    sx_next = __ldg(sx + static_cast<int64_t>(kb + 1) * p.n_tok);
-                    sw_next = __ldg(sw + kb + 1);
+        for (int k = 0; k < C::EC; ++k) acc[k] = 0.0f;
+        for (int it = 0; it < n_kb; ++it) {
+            const int b = it % C::ACCS;
+            if (it % C::FBLK == 0) {
+                // the next FBLK blocks' factors, after everybody has used the last ones
+                const int n = min(C::FBLK, n_kb - it) * NT;
+                if (it > 0) asm volatile("bar.sync 1, %0;" ::"n"(C::EPI_THREADS) : "memory");
+#pragma unroll 4
+                for (int i = e; i < n; i += C::EPI_THREADS) {
+                    const int kb = it + i / NT, t = i % NT;
+                    factors[i] = t0 + t < p.n_tok
+                                     ? __ldg(sx + static_cast<int64_t>(kb) * p.n_tok + t) * __ldg(sw + kb)
+                                     : 0.0f;
                 }
-                if (!f8_warp_wait(&acc_full[b], (it / f8::ACCS) & 1, p.status, abort_flag)) {
-                    stop = true;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t t_col = static_cast<uint32_t>(b * f8::BN + f8::EPI_COLS * half);
-                uint32_t r[f8::EPI_COLS / 32][32];
-#pragma unroll
-                for (int j = 0; j < f8::EPI_COLS / 32; ++j)
-                    tmem_ld_32x32b_x32(tmem_base + t_lane + t_col + 32 * j, r[j]);
-                tmem_ld_wait_for(r[0]);
-#pragma unroll
-                for (int j = 1; j < f8::EPI_COLS / 32; ++j) tmem_ld_use(r[j]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(&acc_empty[b]);
-#pragma unroll
-                for (int j = 0; j < f8::EPI_COLS / 32; ++j) f8_promote<32>(acc + 16 * j, r[j], f32x2(f, f));
+                asm volatile("bar.sync 1, %0;" ::"n"(C::EPI_THREADS) : "memory");
             }
-            if (!stop) f8_store<T, f8::EPI_COLS>(p, row, n0 + f8::EPI_COLS * half, acc);
+            // a wait that gave up sets the flag and lets the loop run out: the barriers above
+            // need every promotion thread
+            if (!*abort_flag) f8_warp_wait(&acc_full[b], (it / C::ACCS) & 1, p.status, abort_flag);
+            tc_fence_after();
+            const uint32_t t_addr = t_addr0 + static_cast<uint32_t>(b * NT);
+            const float* f = factors + (it % C::FBLK) * NT + g * C::EC;
+#pragma unroll
+            for (int j = 0; j < C::EC / 16; ++j) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(t_addr + 16 * j, r);
+                tmem_ld_wait_for(r);
+                if (j == C::EC / 16 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed(&acc_empty[b]);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 f4 = *reinterpret_cast<const float4*>(f + 16 * j + k);
+                    acc[16 * j + k] = fmaf(__uint_as_float(r[k]), f4.x, acc[16 * j + k]);
+                    acc[16 * j + k + 1] = fmaf(__uint_as_float(r[k + 1]), f4.y, acc[16 * j + k + 1]);
+                    acc[16 * j + k + 2] = fmaf(__uint_as_float(r[k + 2]), f4.z, acc[16 * j + k + 2]);
+                    acc[16 * j + k + 3] = fmaf(__uint_as_float(r[k + 3]), f4.w, acc[16 * j + k + 3]);
+                }
+            }
         }
-        __syncwarp();
+        // the ring is free: the last block's MMAs have read their stage. Partial sums [token][channel]
+        float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int k = 0; k < C::EC; ++k) red[(g * C::EC + k) * f8s::BM + 32 * q + lane] = acc[k];
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, f8::TMEM_COLS);
-}
-
-static gptq_status f8_tiles(F8Params& p) {
-    // tile numbers (with a launch's stride added) stay within 31 bits
-    const long long n = static_cast<long long>(p.n_mt) * p.n_nt;
-    if (n > 0x7FFF0000 || f8::BAND * static_cast<long long>(p.n_nt) > 0x7FFF0000) return GPTQ_ERR_ARG;
-    p.n_tiles = static_cast<int>(n);
-    return GPTQ_OK;
-}
-
-template <typename T>
-static gptq_status fp8_gemm_launch(const uint8_t* X8, const uint8_t* W8, F8Params& p,
-                                   cudaStream_t s) {
-    GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, f8::SMEM));
-    CUtensorMap xmap, wmap;
-    GPTQ_TRY(encode_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(X8),
-                                  p.d_in, p.n_tok, p.d_in, f8::BK, f8::BM,
-                                  CU_TENSOR_MAP_SWIZZLE_128B));
-    GPTQ_TRY(encode_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(W8),
-                                  p.d_in, p.d_out, p.d_in, f8::BK, f8::BN,
-                                  CU_TENSOR_MAP_SWIZZLE_128B));
-    p.n_mt = (p.n_tok - 1) / f8::BM + 1;
-    p.n_nt = (p.d_out - 1) / f8::BN + 1;
-    GPTQ_TRY(f8_tiles(p));
-    const int grid = std::min(p.n_tiles, num_sms());
-    fp8_gemm_kernel<T><<<grid, f8::THREADS, f8::SMEM, s>>>(xmap, wmap, p);
-    GPTQ_LAUNCHED();
-    return GPTQ_OK;
+    if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
+    cluster_sync();     // every CTA's partial sums are in its shared memory
+    if (warp >= 3) {
+        // this CTA's share of the tokens: a warp takes a token, a lane four channels
+        const int share = NT / splits, col = c0 + 4 * lane;
+        const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(16 * lane);
+        for (int i = warp - 3; i < share; i += C::EPI_WARPS) {
+            const int t = rank * share + i, row = t0 + t;
+            if (row >= p.n_tok || col >= p.d_out) continue;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < splits; ++r) {
+                const float4 x = ld_cluster_f4(
+                    mapa_shared(mine + static_cast<uint32_t>(t * f8s::BM * 4), static_cast<uint32_t>(r)));
+                v[0] += x.x;
+                v[1] += x.y;
+                v[2] += x.z;
+                v[3] += x.w;
+            }
+            const int64_t off = static_cast<int64_t>(row) * p.d_out + col;
+            const T* R = p.R ? static_cast<const T*>(p.R) + off : nullptr;
+            T* y = static_cast<T*>(p.Y) + off;
+            if (p.vec_ok) {
+                struct alignas(4 * sizeof(T)) Four { T v[4]; };
+                Four o;
+                if (R) {
+                    const Four x = *reinterpret_cast<const Four*>(R);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] += Vec<T>::to_float(x.v[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o.v[j] = Vec<T>::from_float(v[j]);
+                *reinterpret_cast<Four*>(y) = o;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (col + j < p.d_out)
+                        y[j] = Vec<T>::from_float(v[j] + (R ? Vec<T>::to_float(R[j]) : 0.0f));
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();     // no CTA leaves while another may still read its sums
 }
 
 // ---------------------------------------------------------------------------------------
@@ -312,6 +351,7 @@ constexpr int PT = 256;                              // pair tile edge
 constexpr int BM = 128, BNC = 128;                   // tokens, channels loaded per CTA
 constexpr int BK = 128, STAGES = 4;
 constexpr int A_BYTES = BM * BK, STAGE = A_BYTES + BNC * BK;
+constexpr int BAND = 8;                              // token tiles of a band
 constexpr int HN = 128;                              // columns of a promotion warpgroup
 // Warpgroup 0 holds the producer and the two issuers, warpgroups 1 and 2 promote: a
 // thread keeps one token's 128 sums and two 32-column loads in flight, more than an even share
@@ -391,6 +431,18 @@ __device__ __forceinline__ bool f8_store_boxes(const CUtensorMap* ymap, const CU
     return true;
 }
 
+// Tiles run in bands of 8 token tiles with the token tile varying fastest, so the CTAs that run
+// together share weight tiles and activation rows in L2.
+__device__ __forceinline__ void f8_tile(const F8Params& p, int t, int bm, int bn, int& m0,
+                                        int& n0) {
+    const int per_band = f8p::BAND * p.n_nt;
+    const int band = t / per_band;
+    const int rem = t - band * per_band;
+    const int band_m = min(f8p::BAND, p.n_mt - band * f8p::BAND);
+    m0 = (band * f8p::BAND + rem % band_m) * bm;
+    n0 = (rem / band_m) * bn;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(f8p::THREADS, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
@@ -438,6 +490,7 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
     cluster_sync();     // both CTAs' barriers exist before either CTA signals the other's
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
 
     if (warp < f8p::EPI_WARP0) {
         regs_shrink<f8p::REGS_IO>();
@@ -603,6 +656,77 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
     if (warp == 1) tmem_dealloc_pair(tmem_base, f8p::TMEM_COLS);
 }
 
+// `setup` once per device (kernel attributes belong to a device's context).
+template <typename F>
+static gptq_status f8_once(std::atomic<unsigned long long>& done, F&& setup) {
+    int dev = 0;
+    GPTQ_CUDA_TRY(cudaGetDevice(&dev));
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return GPTQ_OK;
+    GPTQ_TRY(setup());
+    done.fetch_or(bit, std::memory_order_release);
+    return GPTQ_OK;
+}
+
+// Launch with clusters of `cluster` CTAs along x, set-up overlapped with the previous kernel's end
+// (the kernels pdl_wait() before they read anything).
+template <typename... KArgs, typename... Args>
+static gptq_status f8_launch(void (*kernel)(KArgs...), int grid, int cluster, int threads, int smem,
+                             cudaStream_t s, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+    GPTQ_LAUNCHED();
+    return GPTQ_OK;
+}
+
+// Ways to split the input channels of `tiles` streaming tiles: as many as fit the GPU at once (where
+// two CTAs share an SM, the last doubling may go past one per SM).
+static int f8_splits(long long tiles, int n_kb, int per_sm) {
+    int splits = 1;
+    while (splits < 8 && 2 * splits <= n_kb &&
+           (per_sm == 2 ? tiles * splits < num_sms() : 2 * tiles * splits <= num_sms()))
+        splits *= 2;
+    return splits;
+}
+
+template <typename T, int NT>
+static gptq_status fp8_stream_launch(const uint8_t* X8, const uint8_t* W8, F8Params& p,
+                                     cudaStream_t s) {
+    using C = f8s::Cfg<NT>;
+    static std::atomic<unsigned long long> done{0};
+    GPTQ_TRY(f8_once(done, []() -> gptq_status {
+        GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_stream_kernel<T, NT>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+        return GPTQ_OK;
+    }));
+    CUtensorMap xmap, wmap;
+    GPTQ_TRY(encode_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(X8),
+                                  p.d_in, p.n_tok, p.d_in, f8s::BK, NT, CU_TENSOR_MAP_SWIZZLE_128B));
+    GPTQ_TRY(encode_tensor_map_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(W8),
+                                  p.d_in, p.d_out, p.d_in, f8s::BK, f8s::BM,
+                                  CU_TENSOR_MAP_SWIZZLE_128B));
+    p.n_mt = (p.n_tok - 1) / NT + 1;
+    p.n_nt = (p.d_out - 1) / f8s::BM + 1;
+    const long long tiles = static_cast<long long>(p.n_mt) * p.n_nt;
+    const int splits = f8_splits(tiles, p.n_kb, C::PER_SM);
+    if (tiles * splits > 0x7FFFFFFF) return GPTQ_ERR_ARG;
+    return f8_launch(fp8_stream_kernel<T, NT>, static_cast<int>(tiles) * splits, splits, C::THREADS,
+                     C::SMEM, s, xmap, wmap, p, splits);
+}
+
 template <typename T>
 struct F8MapType;
 template <>
@@ -621,12 +745,15 @@ struct F8MapType<float> {
 template <typename T>
 static gptq_status fp8_pair_launch(const uint8_t* X8, const uint8_t* W8, F8Params& p,
                                    cudaStream_t s) {
-    GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_pair_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, f8p::SMEM));
-    // the warpgroups' register shares add up to what a launch with REGS per thread has
-    cudaFuncAttributes fa;
-    GPTQ_CUDA_TRY(cudaFuncGetAttributes(&fa, fp8_pair_kernel<T>));
-    if (fa.numRegs < f8p::REGS) return GPTQ_ERR_UNSUPPORTED;
+    static std::atomic<unsigned long long> done{0};
+    GPTQ_TRY(f8_once(done, []() -> gptq_status {
+        GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_pair_kernel<T>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, f8p::SMEM));
+        // the warpgroups' register shares add up to what a launch with REGS per thread has
+        cudaFuncAttributes fa;
+        GPTQ_CUDA_TRY(cudaFuncGetAttributes(&fa, fp8_pair_kernel<T>));
+        return fa.numRegs < f8p::REGS ? GPTQ_ERR_UNSUPPORTED : GPTQ_OK;
+    }));
     CUtensorMap xmap, wmap;
     GPTQ_TRY(encode_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(X8),
                                   p.d_in, p.n_tok, p.d_in, f8p::BK, f8p::BM,
@@ -646,22 +773,13 @@ static gptq_status fp8_pair_launch(const uint8_t* X8, const uint8_t* W8, F8Param
     }
     p.n_mt = (p.n_tok - 1) / f8p::PT + 1;
     p.n_nt = (p.d_out - 1) / f8p::PT + 1;
-    GPTQ_TRY(f8_tiles(p));
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr;
-    cfg.blockDim = dim3(f8p::THREADS);
-    cfg.dynamicSmemBytes = f8p::SMEM;
-    cfg.stream = s;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.n_tiles, num_sms() / 2)));
-    GPTQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T>, xmap, wmap, ymap, rmap, p));
-    GPTQ_LAUNCHED();
-    return GPTQ_OK;
+    // tile numbers (with a launch's stride added) stay within 31 bits
+    const long long tiles = static_cast<long long>(p.n_mt) * p.n_nt;
+    if (tiles > 0x7FFF0000 || f8p::BAND * static_cast<long long>(p.n_nt) > 0x7FFF0000)
+        return GPTQ_ERR_ARG;
+    p.n_tiles = static_cast<int>(tiles);
+    return f8_launch(fp8_pair_kernel<T>, 2 * std::min(p.n_tiles, num_sms() / 2), 2, f8p::THREADS,
+                     f8p::SMEM, s, xmap, wmap, ymap, rmap, p);
 }
 
 template <typename T>
@@ -670,8 +788,22 @@ static gptq_status fp8_linear_launch(const uint8_t* X8, const uint8_t* W8, F8Par
     p.vec_ok = p.d_out % Vec<T>::N == 0;
     const long long pair_tiles = static_cast<long long>((p.n_tok - 1) / f8p::PT + 1) *
                                  ((p.d_out - 1) / f8p::PT + 1);
-    if (p.n_tok > 128 && 2 * pair_tiles >= num_sms()) return fp8_pair_launch<T>(X8, W8, p, s);
-    return fp8_gemm_launch<T>(X8, W8, p, s);
+    if (p.n_tok > 64) {
+        // Blocks of 128 input channels one after the other: a wave of pair tiles takes 0.5 us per
+        // block, a wave of 128 x 128 streaming tiles 0.6 us (measured at d_in 4096 and 11008), so
+        // the streaming kernel is taken where splitting d_in saves more than that (256 tokens,
+        // 11008 -> 4096: 31 us against 49 us; 256 tokens, 4096 -> 11008: 53 us against 23 us).
+        const long long pair_waves = (pair_tiles + num_sms() / 2 - 1) / (num_sms() / 2);
+        const long long tiles = static_cast<long long>((p.n_tok - 1) / 128 + 1) * ((p.d_out - 1) / 128 + 1);
+        const int splits = f8_splits(tiles, p.n_kb, 1);
+        const long long waves = (tiles * splits + num_sms() - 1) / num_sms();
+        if (5 * pair_waves * p.n_kb <= 6 * waves * ((p.n_kb + splits - 1) / splits))
+            return fp8_pair_launch<T>(X8, W8, p, s);
+    }
+    if (p.n_tok <= 16) return fp8_stream_launch<T, 16>(X8, W8, p, s);
+    if (p.n_tok <= 32) return fp8_stream_launch<T, 32>(X8, W8, p, s);
+    if (p.n_tok <= 64) return fp8_stream_launch<T, 64>(X8, W8, p, s);
+    return fp8_stream_launch<T, 128>(X8, W8, p, s);
 }
 
 }  // namespace gq
