@@ -49,12 +49,20 @@ gptq_status encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, vo
 }
 
 gptq_status check_device() {
+    // the answer of each device (1: sm_100, 2: another) is looked up once
+    static std::atomic<int> known[64];
     int dev = 0;
     GPTQ_CUDA_TRY(cudaGetDevice(&dev));
-    int major = 0, minor = 0;
-    GPTQ_CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
-    GPTQ_CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
-    return (major == 10 && minor == 0) ? GPTQ_OK : GPTQ_ERR_UNSUPPORTED;
+    std::atomic<int>& slot = known[dev & 63];
+    int k = dev < 64 ? slot.load(std::memory_order_relaxed) : 0;
+    if (!k) {
+        int major = 0, minor = 0;
+        GPTQ_CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+        GPTQ_CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
+        k = (major == 10 && minor == 0) ? 1 : 2;
+        if (dev < 64) slot.store(k, std::memory_order_relaxed);
+    }
+    return k == 1 ? GPTQ_OK : GPTQ_ERR_UNSUPPORTED;
 }
 
 int num_sms() {

@@ -60,50 +60,65 @@ __device__ __forceinline__ uint32_t amax_vec(const uint4& u, uint32_t m) {
     return m;
 }
 
-// A warp takes 4 tokens x 128 channels: 8 lanes per token, each with C vectors 8*N channels
-// apart, so that every load and store of 8 lanes is one contiguous run.
+// A CTA takes 8 tokens x 1024 channels. A warp takes one token: 8 lanes per 128-channel block, 4
+// blocks per pass, 2 passes, all loads first; a lane's vectors lie 8 vectors apart, so that every
+// load and store of 8 lanes is one contiguous run (a pass of fp16 is 1 KB of one row). The scales
+// leave through shared memory as runs of 8 tokens.
 template <typename T>
 __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, int64_t n, int d,
                                                       uint8_t* __restrict__ codes,
                                                       float* __restrict__ scales) {
-    constexpr int N = Vec<T>::N, C = 128 / (8 * N);
+    constexpr int N = Vec<T>::N, C = 128 / (8 * N), P = 2;
+    __shared__ float sc[4 * P][8];
+    pdl_wait();
     const int lane = lane_id(), part = lane & 7;
     const int nb = (d + 127) / 128;
-    const int64_t n_rb = (n + 31) / 32, units = n_rb * nb;     // 32 tokens x 128 channels
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t rb = u / nb;
-        const int b = static_cast<int>(u - rb * nb);
-        const int64_t t = rb * 32 + warp_id() * 4 + (lane >> 3);
-        uint4 x[C];
-        uint32_t m = 0;
+    const int n_cb = (nb + 4 * P - 1) / (4 * P);
+    const int64_t rb = blockIdx.x / n_cb;
+    const int b0 = static_cast<int>(blockIdx.x - rb * n_cb) * 4 * P + (lane >> 3);
+    const int64_t t = rb * 8 + warp_id();
+    uint4 x[P][C];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int k = b * 128 + (c * 8 + part) * N;
-            x[c] = make_uint4(0, 0, 0, 0);
-            if (t < n && k < d) x[c] = __ldg(reinterpret_cast<const uint4*>(X + t * d + k));
+            const int k = (b0 + 4 * p) * 128 + (c * 8 + part) * N;
+            x[p][c] = make_uint4(0, 0, 0, 0);
+            if (t < n && k < d) x[p][c] = __ldcs(reinterpret_cast<const uint4*>(X + t * d + k));
         }
 #pragma unroll
-        for (int c = 0; c < C; ++c) m = amax_vec<T>(x[c], m);
+    for (int p = 0; p < P; ++p) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) m = amax_vec<T>(x[p][c], m);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const Fp8Scale f = fp8_scale(m);
-        if (t >= n) continue;
+        if (t < n) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = b * 128 + (c * 8 + part) * N;
-            if (k < d) store_codes_vec<T>(codes + t * d + k, x[c], f.r);
+            for (int c = 0; c < C; ++c) {
+                const int k = (b0 + 4 * p) * 128 + (c * 8 + part) * N;
+                if (k < d) store_codes_vec<T>(codes + t * d + k, x[p][c], f.r);
+            }
         }
-        if (part == 0) scales[b * n + t] = f.s;
+        if (part == 0) sc[4 * p + (lane >> 3)][warp_id()] = f.s;
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 * 4 * P) {
+        const int b = static_cast<int>(blockIdx.x - rb * n_cb) * 4 * P + (threadIdx.x >> 3);
+        const int64_t row = rb * 8 + (threadIdx.x & 7);
+        if (b < nb && row < n) scales[b * n + row] = sc[threadIdx.x >> 3][threadIdx.x & 7];
     }
 }
 
 // A block of 256 threads takes one 128 x 128 block: 8 lanes per row, 4 rows per warp and step.
 template <typename T>
-__global__ void __launch_bounds__(256) fp8_weight_kernel(const T* __restrict__ W, int d_out,
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp8_weight_kernel(const T* __restrict__ W, int d_out,
                                                          int d_in, uint8_t* __restrict__ codes,
                                                          float* __restrict__ scales) {
     constexpr int N = Vec<T>::N, C = 128 / (8 * N);
     __shared__ uint32_t warp_max[8];
+    pdl_wait();
     const int lane = lane_id(), part = lane & 7;
     const int nb = (d_in + 127) / 128;
     const int64_t rb = blockIdx.x / nb;
@@ -118,7 +133,7 @@ __global__ void __launch_bounds__(256) fp8_weight_kernel(const T* __restrict__ W
             const int k = b * 128 + (c * 8 + part) * N;
             x[j][c] = make_uint4(0, 0, 0, 0);
             if (row < d_out && k < d_in)
-                x[j][c] = __ldg(reinterpret_cast<const uint4*>(W + row * d_in + k));
+                x[j][c] = __ldcs(reinterpret_cast<const uint4*>(W + row * d_in + k));
         }
     }
 #pragma unroll
@@ -146,9 +161,10 @@ __global__ void __launch_bounds__(256) fp8_weight_kernel(const T* __restrict__ W
 template <typename T>
 static gptq_status fp8_act_launch(const void* X, int64_t n, int d, uint8_t* codes, float* scales,
                                   cudaStream_t s) {
-    const int64_t units = ((n + 31) / 32) * ((d + 127) / 128);
-    const int grid = static_cast<int>(std::min<int64_t>(units, int64_t(1) << 30));
-    fp8_act_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(X), n, d, codes, scales);
+    const int64_t ctas = ((n + 7) / 8) * ((d + 1023) / 1024);
+    if (ctas > 0x7FFFFFFF) return GPTQ_ERR_ARG;
+    GPTQ_CUDA_TRY(launch_pdl(fp8_act_kernel<T>, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s,
+                             static_cast<const T*>(X), n, d, codes, scales));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }
@@ -159,8 +175,8 @@ static gptq_status fp8_weight_launch(const void* W, int d_out, int d_in, uint8_t
     // at most 2^24 row blocks x 512 column blocks
     const int64_t blocks = ((static_cast<int64_t>(d_out) + 127) / 128) * ((d_in + 127) / 128);
     if (blocks > 0x7FFFFFFF) return GPTQ_ERR_ARG;
-    fp8_weight_kernel<T><<<static_cast<int>(blocks), 256, 0, s>>>(static_cast<const T*>(W), d_out,
-                                                                  d_in, codes, scales);
+    GPTQ_CUDA_TRY(launch_pdl(fp8_weight_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                             s, static_cast<const T*>(W), d_out, d_in, codes, scales));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }

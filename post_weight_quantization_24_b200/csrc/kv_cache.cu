@@ -4,8 +4,10 @@
 //
 // Both kernels move each byte once and are bound by HBM (long calls) or by launch latency
 // (a decode step's few tokens). A token's heads lie together in the cache, so its
-// n_heads * head_dim elements are one contiguous row in every array, and the kernels see rows
-// of `width` elements in chunks of 8; a group is 2 to 32 consecutive chunks of one row.
+// n_heads * head_dim elements are one contiguous row in every array. The kernels see plane rows
+// (token 0's keys, token 0's values, token 1's keys, ...) of `wc` chunks of 8 elements; a warp
+// takes 32 consecutive chunks per pass and four passes at a time, whatever the row's width. A group
+// is 2 to 32 consecutive chunks, and never straddles a pass because it divides both.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -18,18 +20,15 @@ struct KvParams {
     int64_t n_slots;       // slots of one plane (keys; the values' plane follows)
     int width, wc;         // elements and 8-element chunks of a token's row
     int ng;                // groups of a row
-    int tpg;               // chunks per group: 2, 4, 8, 16 or 32
+    int tpg_shift;         // log2 of the chunks per group (1 .. 5)
     uint8_t* codes;
     uint16_t* scales;
     uint16_t* zeros;
     int* status;
 };
 
-template <typename T>
-__device__ __forceinline__ void kv_load8(const T* p, float* v) {
-    Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), v);
-    if constexpr (Vec<T>::N == 4) Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(p) + 1), v + 4);
-}
+constexpr int kKvPasses = 4;
+constexpr int kKvThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ void kv_store8(T* p, const float* v) {
@@ -38,147 +37,288 @@ __device__ __forceinline__ void kv_store8(T* p, const float* v) {
 }
 
 constexpr uint16_t kHalfNan = 0x7E00;
+constexpr float kMagicInt = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, half to even
 
-// A thread takes one chunk of 8 elements; the chunks of a token (keys, then values) run over
-// threadIdx.x, tokens over threadIdx.y and the grid. The tpg lanes of a group reduce its range
-// with shuffles, and each computes the group's scalars (fp64, quant.cuh) for its own chunk.
-template <typename T, int BITS>
-__global__ void __launch_bounds__(256) kv_write_kernel(const T* __restrict__ K,
-                                                       const T* __restrict__ V, int64_t n,
-                                                       int64_t k_stride, int64_t v_stride,
-                                                       const int64_t* __restrict__ slots,
-                                                       const KvParams p) {
+// Eight codes of one chunk, packed (BITS == 4: one word; 8: two).
+//   m = v * inv + magic is the nearest integer to v * inv (one rounding), and |v * inv - k| tells how
+//   near v / scale may be to a border: inv is within 2^-23 of 1 / scale and |v / scale| <= 256, so
+//   the quotient is within 2^-15 of v * inv, and only a distance above 1/2 - 1/1024 needs the exact
+//   decision (quant_code). The lower clamp is implied: rint(lo/s) + rint(-lo/s) = 0.
+template <int BITS>
+__device__ __forceinline__ uint2 kv_codes(const float* v, const QParams& g) {
     constexpr int MAXQ = (1 << BITS) - 1;
-    const int chunks = 2 * p.wc;
-    const int64_t t_step = static_cast<int64_t>(gridDim.x) * blockDim.y;
-    // every lane takes every iteration (full-mask shuffles); lanes without work hold zeros
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; t0 < n; t0 += t_step) {
-        const int64_t t = t0 + threadIdx.y;
-        int64_t slot = -1;
-        if (t < n) slot = slots[t];
-        if (slot >= p.n_slots) {
-            if (threadIdx.x == 0) set_status(p.status, GPTQ_ERR_ARG);
-            slot = -1;
+    float m[8], far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = fmaf(v[i], g.inv_scale, kMagicInt);
+        far = fmaxf(far, fabsf(fmaf(v[i], g.inv_scale, kMagicInt - m[i])));
+        m[i] = fminf(m[i] + g.zero, kMagicInt + static_cast<float>(MAXQ));
+    }
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(m[i]);      // 0x4B400000 + code
+    if (!(far <= 0.5f - 1.0f / 1024.0f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(quant_code(v[i], g, MAXQ));
+    }
+    uint2 w;
+    if (BITS == 4) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = (q[2 * i + 1] << 4) + (q[2 * i] & 15u);
+        w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        w.y = 0;
+    } else {
+        w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+        w.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+    }
+    return w;
+}
+
+// Quantise and write. The ranges of a warp's groups are found with shuffles by the TPG lanes of
+// each, but the groups' scalars (fp64, the dearest part: about 100 instructions) are computed by
+// one lane per group for all four passes at once and handed back with shuffles.
+template <typename T, int BITS, int TPG>
+__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restrict__ K,
+                                                              const T* __restrict__ V, int64_t n,
+                                                              int64_t k_stride, int64_t v_stride,
+                                                              const int64_t* __restrict__ slots,
+                                                              const KvParams p, int64_t row_step,
+                                                              int wc_step) {
+    constexpr int MAXQ = (1 << BITS) - 1, U = kKvPasses, VEC = 8 / Vec<T>::N;
+    constexpr int GPP = 32 / TPG;                       // groups of a pass
+    constexpr int UR = U * GPP <= 32 ? U : 32 / GPP;    // passes whose groups fit the lanes
+    pdl_wait();
+    const int lane = lane_id();
+    const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x) >> 5;
+    // this lane's chunk: plane row and chunk of the row
+    int64_t row = warp0 * (32 * U) / p.wc;
+    int wc0 = static_cast<int>(warp0 * (32 * U) - row * p.wc) + lane;
+    while (row < 2 * n) {          // warp-uniform: row and wc0 - lane are the warp's
+        uint4 x[U][VEC];
+        int64_t dst[U];            // slot's row in the cache, or -1
+        int wcs[U];
+        int64_t r = row;
+        int wc = wc0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            while (wc >= p.wc) {
+                wc -= p.wc;
+                ++r;
+            }
+            wcs[u] = wc;
+            dst[u] = -1;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
+            const int64_t t = r >> 1;
+            if (t < n) {
+                const int64_t slot = __ldg(slots + t);
+                const T* src = ((r & 1) ? V + t * v_stride : K + t * k_stride) + 8 * wc;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                if (slot >= 0 && slot < p.n_slots) dst[u] = (r & 1) * p.n_slots + slot;
+                else if (slot >= 0) set_status(p.status, GPTQ_ERR_ARG);
+            }
+            wc += 32;
         }
-        for (int c0 = 0; c0 < chunks; c0 += blockDim.x) {
-            const int c = c0 + threadIdx.x;
-            const bool ok = slot >= 0 && c < chunks;
-            const int plane = c >= p.wc ? 1 : 0;
-            const int wc = c - plane * p.wc;              // chunk of the row
-            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (ok) kv_load8(plane ? V + t * v_stride + 8 * wc : K + t * k_stride + 8 * wc, v);
-            float mn = v[0], mx = v[0];
-            uint32_t am = abs_bits(v[0]);
+        float mn[U], mx[U];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) {
-                mn = fminf(mn, v[i]);
-                mx = fmaxf(mx, v[i]);
-                am = max(am, abs_bits(v[i]));
+        for (int u = 0; u < U; ++u) {
+            vec_minmax(x[u][0], T(), mn[u], mx[u]);
+            if constexpr (VEC == 2) {
+                float a, b;
+                vec_minmax(x[u][1], T(), a, b);
+                mn[u] = min_nan(mn[u], a);
+                mx[u] = max_nan(mx[u], b);
             }
-            for (int o = p.tpg / 2; o > 0; o >>= 1) {
-                mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-            }
-            if (!ok) continue;
-            uint16_t sb = kHalfNan, zb = 0;
-            int q[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (am < kInfBits) {
-                const QParams g = group_params(mn, mx, MAXQ);
-                if (g.scale <= 65504.0f) {
-                    sb = half_bits(g.scale);
-                    zb = half_bits(g.zero);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) q[i] = quant_code(v[i], g, MAXQ);
+            for (int o = TPG / 2; o > 0; o >>= 1) {
+                mn[u] = min_nan(mn[u], __shfl_xor_sync(0xffffffffu, mn[u], o));
+                mx[u] = max_nan(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], o));
+            }
+        }
+#pragma unroll
+        for (int u0 = 0; u0 < U; u0 += UR) {
+            // lane l computes the grid of pass u0 + l / GPP, group l % GPP
+            float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+            for (int u = 0; u < UR; ++u) {
+                const float a = __shfl_sync(0xffffffffu, mn[u0 + u], (lane % GPP) * TPG);
+                const float b = __shfl_sync(0xffffffffu, mx[u0 + u], (lane % GPP) * TPG);
+                if (lane / GPP == u) {
+                    lo = a;
+                    hi = b;
                 }
             }
-            const int64_t row = plane * p.n_slots + slot;
-            if (BITS == 4) {
-                uint32_t w = 0;
+            // (a difference with itself is 0 for finite values only)
+            const bool finite = (lo - lo) == 0.0f && (hi - hi) == 0.0f;
+            QParams mine = group_params(finite ? lo : 0.0f, finite ? hi : 0.0f, MAXQ);
+            if (!finite || !(mine.scale <= 65504.0f)) {
+                mine.scale = __uint_as_float(0x7FC00000u);
+                mine.zero = 0.0f;
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w |= static_cast<uint32_t>(q[i]) << (4 * i);
-                *reinterpret_cast<uint32_t*>(p.codes + (row * p.wc + wc) * 4) = w;
-            } else {
-                uint2 w;
-                w.x = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
-                w.y = q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24);
-                *reinterpret_cast<uint2*>(p.codes + (row * p.wc + wc) * 8) = w;
+            for (int u = u0; u < u0 + UR; ++u) {
+                const int src = (u - u0) * GPP + lane / TPG;
+                QParams g;
+                g.scale = __shfl_sync(0xffffffffu, mine.scale, src);
+                g.zero = __shfl_sync(0xffffffffu, mine.zero, src);
+                g.inv_scale = __shfl_sync(0xffffffffu, mine.inv_scale, src);
+                if (dst[u] < 0) continue;
+                const bool good = g.scale == g.scale;
+                float v[8];
+                Vec<T>::unpack(x[u][0], v);
+                if constexpr (VEC == 2) Vec<T>::unpack(x[u][1], v + 4);
+                uint2 w = make_uint2(0, 0);
+                if (good) w = kv_codes<BITS>(v, g);
+                const int64_t at = dst[u] * p.wc + wcs[u];
+                if (BITS == 4) reinterpret_cast<uint32_t*>(p.codes)[at] = w.x;
+                else reinterpret_cast<uint2*>(p.codes)[at] = w;
+                if (lane % TPG == 0) {
+                    const int64_t gi = dst[u] * p.ng + wcs[u] / TPG;
+                    p.scales[gi] = good ? half_bits(g.scale) : kHalfNan;
+                    p.zeros[gi] = half_bits(g.zero);
+                }
             }
-            if ((wc & (p.tpg - 1)) == 0) {
-                const int64_t gi = row * p.ng + wc / p.tpg;
-                p.scales[gi] = sb;
-                p.zeros[gi] = zb;
-            }
+        }
+        // the warp's next 128 chunks
+        row += row_step;
+        wc0 += wc_step;
+        if (wc0 - lane >= p.wc) {
+            wc0 -= p.wc;
+            ++row;
         }
     }
 }
 
-// The sequence of row t: the largest b with cu[b] <= t, by a 32-way search of the warp (-1 when
-// t < cu[0]).
+// The largest b in [0, n_seqs] with cu[b] <= t; -1 when t < cu[0].
 __device__ __forceinline__ int kv_find_seq(const int32_t* __restrict__ cu, int n_seqs, int64_t t) {
-    int lo = 0, count = n_seqs + 1;               // cu[lo .. lo + count) holds the answer
-    while (count > 0) {
-        const int step = (count + 31) / 32;
-        const int i = lo + lane_id() * step;
-        const bool below = lane_id() * step < count && __ldg(cu + i) <= t;
-        const int k = __popc(__ballot_sync(0xffffffffu, below));
-        if (k == 0) return lo - 1;                // only in the first round, or none further on
-        const int end = lo + count;
-        lo += (k - 1) * step;
-        if (step == 1) return lo;
-        // cu[lo] <= t: look among the entries behind it, up to the next probe
-        ++lo;
-        count = min(step - 1, end - lo);
+    int lo = -1, hi = n_seqs + 1;              // cu[lo] <= t < cu[hi] (virtually, at the ends)
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (__ldg(cu + mid) <= t) lo = mid;
+        else hi = mid;
     }
-    return lo - 1;
+    return lo;
 }
 
-// A warp takes one row of the output (a token's keys and values); lanes run over its chunks.
+// Eight values of one chunk. A code becomes the fp32 2^23 + code by placing its byte into a
+// constant; the difference to 2^23 + zero is exact, and so is the product with the fp16 scale.
+template <int BITS>
+__device__ __forceinline__ void kv_values(uint2 w, float scale, float zero, float* v) {
+    const float z = 8388608.0f + zero;
+    uint32_t a = w.x, b = w.y;
+    if (BITS == 4) {
+        b = (w.x >> 4) & 0x0F0F0F0Fu;          // odd elements
+        a = w.x & 0x0F0F0F0Fu;                 // even elements
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = __uint_as_float(__byte_perm(a, 0x4B000000u, 0x7540 + i));
+        const float y = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 + i));
+        v[BITS == 4 ? 2 * i : i] = scale * (x - z);
+        v[BITS == 4 ? 2 * i + 1 : 4 + i] = scale * (y - z);
+    }
+}
+
+// Read back. A warp takes `rows` (1 to 32) consecutive tokens: lane i finds token i's sequence,
+// page and slot, and the warp then runs over the tokens' chunks, four passes of loads at a time.
 template <typename T, int BITS>
-__global__ void __launch_bounds__(256) kv_read_kernel(const KvParams p, int page_size,
-                                                      int64_t n_pages,
-                                                      const int32_t* __restrict__ table,
-                                                      int n_seqs, int max_pages,
-                                                      const int32_t* __restrict__ cu,
-                                                      int64_t total, T* __restrict__ K,
-                                                      T* __restrict__ V) {
-    const int lane = lane_id(), chunks = 2 * p.wc;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp_id(); t < total; t += step) {
-        const int b = kv_find_seq(cu, n_seqs, t);
-        if (b < 0 || b >= n_seqs) continue;       // a row of no sequence: left as it was
-        const int64_t pos = t - __ldg(cu + b);
-        const int64_t pi = pos / page_size;
-        int64_t page = -1;
-        if (pos >= 0 && pi < max_pages) page = __ldg(table + static_cast<int64_t>(b) * max_pages + pi);
-        const bool found = page >= 0 && page < n_pages;
-        if (!found && lane == 0) set_status(p.status, GPTQ_ERR_ARG);
-        const int64_t slot = page * page_size + (pos - pi * page_size);
-#pragma unroll 4
-        for (int c = lane; c < chunks; c += 32) {
-            const int plane = c >= p.wc ? 1 : 0;
-            const int wc = c - plane * p.wc;
-            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (found) {
-                const int64_t row = plane * p.n_slots + slot;
-                const int64_t gi = row * p.ng + wc / p.tpg;
-                const float s = __half2float(__ushort_as_half(__ldg(p.scales + gi)));
-                const float z = __half2float(__ushort_as_half(__ldg(p.zeros + gi)));
-                if (BITS == 4) {
-                    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p.codes) + row * p.wc + wc);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = s * (static_cast<float>((w >> (4 * i)) & 15u) - z);
-                } else {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.codes) + row * p.wc + wc);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = s * (static_cast<float>((w.x >> (8 * i)) & 255u) - z);
-                        v[4 + i] = s * (static_cast<float>((w.y >> (8 * i)) & 255u) - z);
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, int page_size,
+                                                             int64_t n_pages,
+                                                             const int32_t* __restrict__ table,
+                                                             int n_seqs, int max_pages,
+                                                             const int32_t* __restrict__ cu,
+                                                             int64_t total, int rows,
+                                                             T* __restrict__ K, T* __restrict__ V) {
+    constexpr int U = kKvPasses;
+    constexpr int64_t kNobody = -2, kMissing = -1;
+    pdl_wait();
+    const int lane = lane_id();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kKvThreads / 32) * rows;
+    for (int64_t t0 = ((static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x) >> 5) * rows;
+         t0 < total; t0 += step) {
+        int64_t mine = kNobody;
+        if (lane < rows && t0 + lane < total) {
+            const int b = kv_find_seq(cu, n_seqs, t0 + lane);
+            if (b >= 0 && b < n_seqs) {        // else a row of no sequence: left as it was
+                const int64_t pos = t0 + lane - __ldg(cu + b);
+                mine = kMissing;
+                if (pos >= 0) {
+                    const unsigned pi = static_cast<unsigned>(pos) / static_cast<unsigned>(page_size);
+                    if (pi < static_cast<unsigned>(max_pages)) {
+                        const int64_t page = __ldg(table + static_cast<int64_t>(b) * max_pages + pi);
+                        if (page >= 0 && page < n_pages)
+                            mine = page * page_size + (pos - static_cast<int64_t>(pi) * page_size);
                     }
                 }
+                if (mine == kMissing) set_status(p.status, GPTQ_ERR_ARG);
             }
-            kv_store8((plane ? V : K) + t * p.width + 8 * wc, v);
         }
+        const int n_rows = 2 * static_cast<int>(min(static_cast<int64_t>(rows), total - t0));
+        int r = 0, wc = lane;                  // plane row (token, keys or values) and its chunk
+        for (int base = 0; base < n_rows * p.wc; base += 32 * U) {
+            uint2 w[U];
+            uint16_t sb[U], zb[U];
+            int rr[U], cc[U];
+            int64_t slot[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                while (wc >= p.wc) {
+                    wc -= p.wc;
+                    ++r;
+                }
+                rr[u] = r;
+                cc[u] = wc;
+                slot[u] = __shfl_sync(0xffffffffu, mine, (r >> 1) & 31);
+                if (r >= n_rows) slot[u] = kNobody;
+                w[u] = make_uint2(0, 0);
+                sb[u] = zb[u] = 0;
+                if (slot[u] >= 0) {
+                    const int64_t row = (r & 1) * p.n_slots + slot[u];
+                    const int64_t gi = row * p.ng + (wc >> p.tpg_shift);
+                    if (BITS == 4) w[u].x = __ldg(reinterpret_cast<const uint32_t*>(p.codes) + row * p.wc + wc);
+                    else w[u] = __ldg(reinterpret_cast<const uint2*>(p.codes) + row * p.wc + wc);
+                    sb[u] = __ldg(p.scales + gi);
+                    zb[u] = __ldg(p.zeros + gi);
+                }
+                wc += 32;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (slot[u] == kNobody) continue;
+                float v[8];
+                kv_values<BITS>(w[u], __half2float(__ushort_as_half(sb[u])),
+                                __half2float(__ushort_as_half(zb[u])), v);
+                kv_store8(((rr[u] & 1) ? V : K) + (t0 + (rr[u] >> 1)) * p.width + 8 * cc[u], v);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T, int BITS, int TPG>
+static gptq_status kv_write_go(const T* K, const T* V, int64_t n, int64_t ks, int64_t vs,
+                               const int64_t* slots, const KvParams& p, cudaStream_t s) {
+    constexpr int64_t kChunks = 32 * kKvPasses * (kKvThreads / 32);       // of a CTA
+    const int64_t want = (2 * n * p.wc + kChunks - 1) / kChunks;
+    const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 16));
+    const int64_t stride = grid * kChunks;
+    GPTQ_CUDA_TRY(launch_pdl(kv_write_kernel<T, BITS, TPG>, dim3(grid), dim3(kKvThreads), 0, s, K, V,
+                             n, ks, vs, slots, p, stride / p.wc, static_cast<int>(stride % p.wc)));
+    GPTQ_LAUNCHED();
+    return GPTQ_OK;
+}
+
+template <typename T, int BITS>
+static gptq_status kv_write_group(const T* K, const T* V, int64_t n, int64_t ks, int64_t vs,
+                                  const int64_t* slots, const KvParams& p, cudaStream_t s) {
+    switch (p.tpg_shift) {
+        case 1: return kv_write_go<T, BITS, 2>(K, V, n, ks, vs, slots, p, s);
+        case 2: return kv_write_go<T, BITS, 4>(K, V, n, ks, vs, slots, p, s);
+        case 3: return kv_write_go<T, BITS, 8>(K, V, n, ks, vs, slots, p, s);
+        case 4: return kv_write_go<T, BITS, 16>(K, V, n, ks, vs, slots, p, s);
+        default: return kv_write_go<T, BITS, 32>(K, V, n, ks, vs, slots, p, s);
     }
 }
 
@@ -186,19 +326,10 @@ template <typename T>
 static gptq_status kv_write_launch(const void* K, const void* V, int64_t n, int64_t ks, int64_t vs,
                                    const int64_t* slots, int bits, const KvParams& p,
                                    cudaStream_t s) {
-    int bx = 32;
-    while (bx < 2 * p.wc && bx < 256) bx *= 2;
-    const dim3 block(bx, 256 / bx);
-    const int64_t want = (n + block.y - 1) / block.y;
-    const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 64));
     const T* k = static_cast<const T*>(K);
     const T* v = static_cast<const T*>(V);
-    if (bits == 4)
-        kv_write_kernel<T, 4><<<grid, block, 0, s>>>(k, v, n, ks, vs, slots, p);
-    else
-        kv_write_kernel<T, 8><<<grid, block, 0, s>>>(k, v, n, ks, vs, slots, p);
-    GPTQ_LAUNCHED();
-    return GPTQ_OK;
+    return bits == 4 ? kv_write_group<T, 4>(k, v, n, ks, vs, slots, p, s)
+                     : kv_write_group<T, 8>(k, v, n, ks, vs, slots, p, s);
 }
 
 template <typename T>
@@ -206,16 +337,21 @@ static gptq_status kv_read_launch(const KvParams& p, int page_size, int64_t n_pa
                                   const int32_t* table, int n_seqs, int max_pages,
                                   const int32_t* cu, int64_t total, void* K, void* V, int bits,
                                   cudaStream_t s) {
-    const int64_t want = (total + 7) / 8;
+    // tokens per warp: up to 32, so that a search is shared, but fewer while warps are scarce
+    const int64_t warps = static_cast<int64_t>(num_sms()) * 32;
+    int rows = 1;
+    while (rows < 32 && 2 * rows * warps <= total) rows *= 2;
+    const int64_t per_cta = rows * (kKvThreads / 32);
+    const int64_t want = (total + per_cta - 1) / per_cta;
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 64));
     T* k = static_cast<T*>(K);
     T* v = static_cast<T*>(V);
     if (bits == 4)
-        kv_read_kernel<T, 4><<<grid, 256, 0, s>>>(p, page_size, n_pages, table, n_seqs, max_pages,
-                                                  cu, total, k, v);
+        GPTQ_CUDA_TRY(launch_pdl(kv_read_kernel<T, 4>, dim3(grid), dim3(kKvThreads), 0, s, p, page_size,
+                                 n_pages, table, n_seqs, max_pages, cu, total, rows, k, v));
     else
-        kv_read_kernel<T, 8><<<grid, 256, 0, s>>>(p, page_size, n_pages, table, n_seqs, max_pages,
-                                                  cu, total, k, v);
+        GPTQ_CUDA_TRY(launch_pdl(kv_read_kernel<T, 8>, dim3(grid), dim3(kKvThreads), 0, s, p, page_size,
+                                 n_pages, table, n_seqs, max_pages, cu, total, rows, k, v));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }
@@ -243,7 +379,8 @@ static gptq_status kv_params(int dtype, int n_heads, int head_dim, int bits, int
     p->width = n_heads * head_dim;
     p->wc = p->width / 8;
     p->ng = p->width / group_size;
-    p->tpg = group_size / 8;
+    p->tpg_shift = 1;
+    while ((16 << (p->tpg_shift - 1)) < group_size) ++p->tpg_shift;
     p->codes = static_cast<uint8_t*>(const_cast<void*>(codes));
     p->scales = static_cast<uint16_t*>(const_cast<void*>(scales));
     p->zeros = static_cast<uint16_t*>(const_cast<void*>(zeros));
