@@ -6,8 +6,11 @@
 // (a decode step's few tokens). A token's heads lie together in the cache, so its
 // n_heads * head_dim elements are one contiguous row in every array. The kernels see plane rows
 // (token 0's keys, token 0's values, token 1's keys, ...) of `wc` chunks of 8 elements; a warp
-// takes 32 consecutive chunks per pass and four passes at a time, whatever the row's width. A group
-// is 2 to 32 consecutive chunks, and never straddles a pass because it divides both.
+// takes 32 consecutive chunks per pass. Where rows are whole multiples of 128 chunks (1024
+// elements), it takes four passes of one row at a time (U = 4), which shares a row's addresses and
+// a group's scalars among them and keeps 64 bytes per lane in flight; other widths go pass by
+// pass over row ends (U = 1). A group is 2 to 32 consecutive chunks and never straddles a pass,
+// because it divides both.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -27,7 +30,6 @@ struct KvParams {
     int* status;
 };
 
-constexpr int kKvPasses = 4;
 constexpr int kKvThreads = 128;
 
 template <typename T>
@@ -78,48 +80,48 @@ __device__ __forceinline__ uint2 kv_codes(const float* v, const QParams& g) {
 // Quantise and write. The ranges of a warp's groups are found with shuffles by the TPG lanes of
 // each, but the groups' scalars (fp64, the dearest part: about 100 instructions) are computed by
 // one lane per group for all four passes at once and handed back with shuffles.
-template <typename T, int BITS, int TPG>
+template <typename T, int BITS, int TPG, int U>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restrict__ K,
                                                               const T* __restrict__ V, int64_t n,
                                                               int64_t k_stride, int64_t v_stride,
                                                               const int64_t* __restrict__ slots,
                                                               const KvParams p, int64_t row_step,
                                                               int wc_step) {
-    constexpr int MAXQ = (1 << BITS) - 1, U = kKvPasses, VEC = 8 / Vec<T>::N;
+    constexpr int MAXQ = (1 << BITS) - 1, VEC = 8 / Vec<T>::N;
     constexpr int GPP = 32 / TPG;                       // groups of a pass
     constexpr int UR = U * GPP <= 32 ? U : 32 / GPP;    // passes whose groups fit the lanes
     pdl_wait();
     const int lane = lane_id();
     const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x) >> 5;
-    // this lane's chunk: plane row and chunk of the row
-    int64_t row = warp0 * (32 * U) / p.wc;
-    int wc0 = static_cast<int>(warp0 * (32 * U) - row * p.wc) + lane;
-    while (row < 2 * n) {          // warp-uniform: row and wc0 - lane are the warp's
-        uint4 x[U][VEC];
-        int64_t dst[U];            // slot's row in the cache, or -1
-        int wcs[U];
+    int64_t row = warp0 * (32 * U) / p.wc;              // the warp's plane row and first chunk
+    int wc0 = static_cast<int>(warp0 * (32 * U) - row * p.wc);
+    while (row < 2 * n) {                               // warp-uniform
         int64_t r = row;
-        int wc = wc0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
+        int wc = wc0 + lane;
+        if (U == 1) {                                   // a pass may run over row ends
             while (wc >= p.wc) {
                 wc -= p.wc;
                 ++r;
             }
-            wcs[u] = wc;
-            dst[u] = -1;
+        }
+        const int64_t t = r >> 1;
+        const bool is_v = r & 1;
+        int64_t dst = -1;                               // the slot's row in the cache, or -1
+        uint4 x[U][VEC];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
-            const int64_t t = r >> 1;
-            if (t < n) {
-                const int64_t slot = __ldg(slots + t);
-                const T* src = ((r & 1) ? V + t * v_stride : K + t * k_stride) + 8 * wc;
+        if (U > 1 || t < n) {
+            const int64_t slot = __ldg(slots + t);
+            const uint4* src = reinterpret_cast<const uint4*>(
+                (is_v ? V + t * v_stride : K + t * k_stride) + 8 * wc);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-                if (slot >= 0 && slot < p.n_slots) dst[u] = (r & 1) * p.n_slots + slot;
-                else if (slot >= 0) set_status(p.status, GPTQ_ERR_ARG);
-            }
-            wc += 32;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) x[u][i] = __ldcs(src + u * 32 * VEC + i);
+            if (slot >= 0 && slot < p.n_slots) dst = (is_v ? p.n_slots : 0) + slot;
+            else if (slot >= 0) set_status(p.status, GPTQ_ERR_ARG);
         }
         float mn[U], mx[U];
 #pragma unroll
@@ -164,27 +166,26 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
                 g.scale = __shfl_sync(0xffffffffu, mine.scale, src);
                 g.zero = __shfl_sync(0xffffffffu, mine.zero, src);
                 g.inv_scale = __shfl_sync(0xffffffffu, mine.inv_scale, src);
-                if (dst[u] < 0) continue;
+                if (dst < 0) continue;
                 const bool good = g.scale == g.scale;
                 float v[8];
                 Vec<T>::unpack(x[u][0], v);
                 if constexpr (VEC == 2) Vec<T>::unpack(x[u][1], v + 4);
                 uint2 w = make_uint2(0, 0);
                 if (good) w = kv_codes<BITS>(v, g);
-                const int64_t at = dst[u] * p.wc + wcs[u];
+                const int64_t at = dst * p.wc + wc + 32 * u;
                 if (BITS == 4) reinterpret_cast<uint32_t*>(p.codes)[at] = w.x;
                 else reinterpret_cast<uint2*>(p.codes)[at] = w;
                 if (lane % TPG == 0) {
-                    const int64_t gi = dst[u] * p.ng + wcs[u] / TPG;
+                    const int64_t gi = dst * p.ng + (wc + 32 * u) / TPG;
                     p.scales[gi] = good ? half_bits(g.scale) : kHalfNan;
                     p.zeros[gi] = half_bits(g.zero);
                 }
             }
         }
-        // the warp's next 128 chunks
         row += row_step;
         wc0 += wc_step;
-        if (wc0 - lane >= p.wc) {
+        if (wc0 >= p.wc) {
             wc0 -= p.wc;
             ++row;
         }
@@ -223,7 +224,7 @@ __device__ __forceinline__ void kv_values(uint2 w, float scale, float zero, floa
 
 // Read back. A warp takes `rows` (1 to 32) consecutive tokens: lane i finds token i's sequence,
 // page and slot, and the warp then runs over the tokens' chunks, four passes of loads at a time.
-template <typename T, int BITS>
+template <typename T, int BITS, int U>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, int page_size,
                                                              int64_t n_pages,
                                                              const int32_t* __restrict__ table,
@@ -231,7 +232,6 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
                                                              const int32_t* __restrict__ cu,
                                                              int64_t total, int rows,
                                                              T* __restrict__ K, T* __restrict__ V) {
-    constexpr int U = kKvPasses;
     constexpr int64_t kNobody = -2, kMissing = -1;
     pdl_wait();
     const int lane = lane_id();
@@ -258,67 +258,65 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
         const int n_rows = 2 * static_cast<int>(min(static_cast<int64_t>(rows), total - t0));
         int r = 0, wc = lane;                  // plane row (token, keys or values) and its chunk
         for (int base = 0; base < n_rows * p.wc; base += 32 * U) {
-            uint2 w[U];
-            uint16_t sb[U], zb[U];
-            int rr[U], cc[U];
-            int64_t slot[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                while (wc >= p.wc) {
-                    wc -= p.wc;
-                    ++r;
-                }
-                rr[u] = r;
-                cc[u] = wc;
-                slot[u] = __shfl_sync(0xffffffffu, mine, (r >> 1) & 31);
-                if (r >= n_rows) slot[u] = kNobody;
-                w[u] = make_uint2(0, 0);
-                sb[u] = zb[u] = 0;
-                if (slot[u] >= 0) {
-                    const int64_t row = (r & 1) * p.n_slots + slot[u];
-                    const int64_t gi = row * p.ng + (wc >> p.tpg_shift);
-                    if (BITS == 4) w[u].x = __ldg(reinterpret_cast<const uint32_t*>(p.codes) + row * p.wc + wc);
-                    else w[u] = __ldg(reinterpret_cast<const uint2*>(p.codes) + row * p.wc + wc);
-                    sb[u] = __ldg(p.scales + gi);
-                    zb[u] = __ldg(p.zeros + gi);
-                }
-                wc += 32;
+            while (wc >= p.wc) {
+                wc -= p.wc;
+                ++r;
             }
+            const int64_t slot = __shfl_sync(0xffffffffu, mine, (r >> 1) & 31);
+            if (r < n_rows && slot != kNobody) {
+                uint2 w[U];
+                uint16_t sb[U], zb[U];
+                const int64_t row = ((r & 1) ? p.n_slots : 0) + slot;
+                const int64_t c0 = row * p.wc + wc, g0 = row * p.ng + (wc >> p.tpg_shift);
+                const int g_step = 32 >> p.tpg_shift;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (slot[u] == kNobody) continue;
-                float v[8];
-                kv_values<BITS>(w[u], __half2float(__ushort_as_half(sb[u])),
-                                __half2float(__ushort_as_half(zb[u])), v);
-                kv_store8(((rr[u] & 1) ? V : K) + (t0 + (rr[u] >> 1)) * p.width + 8 * cc[u], v);
+                for (int u = 0; u < U; ++u) {
+                    w[u] = make_uint2(0, 0);
+                    sb[u] = zb[u] = 0;
+                    if (slot >= 0) {
+                        if (BITS == 4) w[u].x = __ldg(reinterpret_cast<const uint32_t*>(p.codes) + c0 + 32 * u);
+                        else w[u] = __ldg(reinterpret_cast<const uint2*>(p.codes) + c0 + 32 * u);
+                        sb[u] = __ldg(p.scales + g0 + u * g_step);
+                        zb[u] = __ldg(p.zeros + g0 + u * g_step);
+                    }
+                }
+                T* out = ((r & 1) ? V : K) + (t0 + (r >> 1)) * p.width + 8 * wc;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float v[8];
+                    kv_values<BITS>(w[u], __half2float(__ushort_as_half(sb[u])),
+                                    __half2float(__ushort_as_half(zb[u])), v);
+                    kv_store8(out + 256 * u, v);
+                }
             }
+            wc += 32 * U;
         }
         __syncwarp();
     }
 }
 
-template <typename T, int BITS, int TPG>
+template <typename T, int BITS, int TPG, int U>
 static gptq_status kv_write_go(const T* K, const T* V, int64_t n, int64_t ks, int64_t vs,
                                const int64_t* slots, const KvParams& p, cudaStream_t s) {
-    constexpr int64_t kChunks = 32 * kKvPasses * (kKvThreads / 32);       // of a CTA
+    constexpr int64_t kChunks = 32 * U * (kKvThreads / 32);       // of a CTA
     const int64_t want = (2 * n * p.wc + kChunks - 1) / kChunks;
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 16));
     const int64_t stride = grid * kChunks;
-    GPTQ_CUDA_TRY(launch_pdl(kv_write_kernel<T, BITS, TPG>, dim3(grid), dim3(kKvThreads), 0, s, K, V,
+    GPTQ_CUDA_TRY(launch_pdl(kv_write_kernel<T, BITS, TPG, U>, dim3(grid), dim3(kKvThreads), 0, s, K, V,
                              n, ks, vs, slots, p, stride / p.wc, static_cast<int>(stride % p.wc)));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }
 
-template <typename T, int BITS>
+template <typename T, int BITS, int U>
 static gptq_status kv_write_group(const T* K, const T* V, int64_t n, int64_t ks, int64_t vs,
                                   const int64_t* slots, const KvParams& p, cudaStream_t s) {
     switch (p.tpg_shift) {
-        case 1: return kv_write_go<T, BITS, 2>(K, V, n, ks, vs, slots, p, s);
-        case 2: return kv_write_go<T, BITS, 4>(K, V, n, ks, vs, slots, p, s);
-        case 3: return kv_write_go<T, BITS, 8>(K, V, n, ks, vs, slots, p, s);
-        case 4: return kv_write_go<T, BITS, 16>(K, V, n, ks, vs, slots, p, s);
-        default: return kv_write_go<T, BITS, 32>(K, V, n, ks, vs, slots, p, s);
+        case 1: return kv_write_go<T, BITS, 2, U>(K, V, n, ks, vs, slots, p, s);
+        case 2: return kv_write_go<T, BITS, 4, U>(K, V, n, ks, vs, slots, p, s);
+        case 3: return kv_write_go<T, BITS, 8, U>(K, V, n, ks, vs, slots, p, s);
+        case 4: return kv_write_go<T, BITS, 16, U>(K, V, n, ks, vs, slots, p, s);
+        default: return kv_write_go<T, BITS, 32, U>(K, V, n, ks, vs, slots, p, s);
     }
 }
 
@@ -328,8 +326,11 @@ static gptq_status kv_write_launch(const void* K, const void* V, int64_t n, int6
                                    cudaStream_t s) {
     const T* k = static_cast<const T*>(K);
     const T* v = static_cast<const T*>(V);
-    return bits == 4 ? kv_write_group<T, 4>(k, v, n, ks, vs, slots, p, s)
-                     : kv_write_group<T, 8>(k, v, n, ks, vs, slots, p, s);
+    if (p.wc % 128 == 0)
+        return bits == 4 ? kv_write_group<T, 4, 4>(k, v, n, ks, vs, slots, p, s)
+                         : kv_write_group<T, 8, 4>(k, v, n, ks, vs, slots, p, s);
+    return bits == 4 ? kv_write_group<T, 4, 1>(k, v, n, ks, vs, slots, p, s)
+                     : kv_write_group<T, 8, 1>(k, v, n, ks, vs, slots, p, s);
 }
 
 template <typename T>
@@ -346,12 +347,11 @@ static gptq_status kv_read_launch(const KvParams& p, int page_size, int64_t n_pa
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 64));
     T* k = static_cast<T*>(K);
     T* v = static_cast<T*>(V);
-    if (bits == 4)
-        GPTQ_CUDA_TRY(launch_pdl(kv_read_kernel<T, 4>, dim3(grid), dim3(kKvThreads), 0, s, p, page_size,
-                                 n_pages, table, n_seqs, max_pages, cu, total, rows, k, v));
-    else
-        GPTQ_CUDA_TRY(launch_pdl(kv_read_kernel<T, 8>, dim3(grid), dim3(kKvThreads), 0, s, p, page_size,
-                                 n_pages, table, n_seqs, max_pages, cu, total, rows, k, v));
+    auto* kernel = p.wc % 128 == 0
+                       ? (bits == 4 ? kv_read_kernel<T, 4, 4> : kv_read_kernel<T, 8, 4>)
+                       : (bits == 4 ? kv_read_kernel<T, 4, 1> : kv_read_kernel<T, 8, 1>);
+    GPTQ_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kKvThreads), 0, s, p, page_size, n_pages, table,
+                             n_seqs, max_pages, cu, total, rows, k, v));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }
