@@ -41,40 +41,54 @@ __device__ __forceinline__ void kv_store8(T* p, const float* v) {
 constexpr uint16_t kHalfNan = 0x7E00;
 constexpr float kMagicInt = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, half to even
 
-// Eight codes of one chunk, packed (BITS == 4: one word; 8: two).
-//   m = v * inv + magic is the nearest integer to v * inv (one rounding), and |v * inv - k| tells how
-//   near v / scale may be to a border: inv is within 2^-23 of 1 / scale and |v / scale| <= 256, so
-//   the quotient is within 2^-15 of v * inv, and only a distance above 1/2 - 1/1024 needs the exact
-//   decision (quant_code). The lower clamp is implied: rint(lo/s) + rint(-lo/s) = 0.
+// Four codes' bytes (each the low byte of its word) in one word.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Eight codes (in the low bits of each q) packed, BITS == 4: one word; 8: two.
+template <int BITS>
+__device__ __forceinline__ uint2 pack_codes(const uint32_t* q) {
+    if (BITS == 4)
+        return make_uint2(low_bytes((q[1] << 4) + (q[0] & 15u), (q[3] << 4) + (q[2] & 15u),
+                                    (q[5] << 4) + (q[4] & 15u), (q[7] << 4) + (q[6] & 15u)),
+                          0);
+    return make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
+}
+
+// The exact decision for all eight, out of line: few chunks need it.
+template <int BITS>
+__device__ __noinline__ uint2 kv_codes_exact(float4 a, float4 b, float scale, float zero, float inv) {
+    const QParams g{scale, zero, inv};
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(quant_code(v[i], g, (1 << BITS) - 1));
+    return pack_codes<BITS>(q);
+}
+
+// Eight codes of one chunk. m = v * inv + magic holds the integer nearest to v * inv (one rounding).
+// inv is 1 / scale to 2^-24 and |v / scale| <= MAXQ, so the quotient is within (MAXQ + 1) * 2^-24 of
+// v * inv, and only where v * inv is nearer than 4 times that to a border is the exact decision
+// needed (one chunk in 4000 of 4 bits, in 500 of 8). The lower clamp is implied:
+// rint(lo/s) + rint(-lo/s) = 0.
 template <int BITS>
 __device__ __forceinline__ uint2 kv_codes(const float* v, const QParams& g) {
     constexpr int MAXQ = (1 << BITS) - 1;
-    float m[8], far = 0.0f;
+    constexpr float kNear = 0.5f - (MAXQ + 1) * 0x1p-22f;
+    uint32_t q[8];
+    float far = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        m[i] = fmaf(v[i], g.inv_scale, kMagicInt);
-        far = fmaxf(far, fabsf(fmaf(v[i], g.inv_scale, kMagicInt - m[i])));
-        m[i] = fminf(m[i] + g.zero, kMagicInt + static_cast<float>(MAXQ));
+        const float m = fmaf(v[i], g.inv_scale, kMagicInt);
+        far = fmaxf(far, fabsf(fmaf(v[i], g.inv_scale, kMagicInt - m)));
+        q[i] = __float_as_uint(fminf(m + g.zero, kMagicInt + static_cast<float>(MAXQ)));
     }
-    uint32_t q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(m[i]);      // 0x4B400000 + code
-    if (!(far <= 0.5f - 1.0f / 1024.0f)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(quant_code(v[i], g, MAXQ));
-    }
-    uint2 w;
-    if (BITS == 4) {
-        uint32_t b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = (q[2 * i + 1] << 4) + (q[2 * i] & 15u);
-        w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-        w.y = 0;
-    } else {
-        w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-        w.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-    }
-    return w;
+    if (far > kNear)
+        return kv_codes_exact<BITS>(make_float4(v[0], v[1], v[2], v[3]),
+                                    make_float4(v[4], v[5], v[6], v[7]), g.scale, g.zero,
+                                    g.inv_scale);
+    return pack_codes<BITS>(q);
 }
 
 // Quantise and write. The ranges of a warp's groups are found with shuffles by the TPG lanes of
