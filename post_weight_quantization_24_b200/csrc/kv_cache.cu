@@ -6,10 +6,10 @@
 // (a decode step's few tokens). A token's heads lie together in the cache, so its
 // n_heads * head_dim elements are one contiguous row in every array. The kernels see plane rows
 // (token 0's keys, token 0's values, token 1's keys, ...) of `wc` chunks of 8 elements; a warp
-// takes 32 consecutive chunks per pass. Where rows are whole multiples of 128 chunks (1024
-// elements), it takes four passes of one row at a time (U = 4), which shares a row's addresses and
-// a group's scalars among them and keeps 64 bytes per lane in flight; other widths go pass by
-// pass over row ends (U = 1). A group is 2 to 32 consecutive chunks and never straddles a pass,
+// takes 32 consecutive chunks per pass. Where rows are whole multiples of 128 or 64 chunks (1024 or
+// 512 elements), it takes four or two passes of one row at a time (U), which shares a row's
+// addresses among them and the work on the groups' scalars, and keeps 16 U bytes per lane in
+// flight; other widths go pass by pass over row ends (U = 1). A group is 2 to 32 consecutive chunks and never straddles a pass,
 // because it divides both.
 #include <algorithm>
 
@@ -41,55 +41,113 @@ __device__ __forceinline__ void kv_store8(T* p, const float* v) {
 constexpr uint16_t kHalfNan = 0x7E00;
 constexpr float kMagicInt = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, half to even
 
-// Four codes' bytes (each the low byte of its word) in one word.
-__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-}
+// A group's grid as the code loop uses it: 1/scale a little up and down, and what turns the bits of
+// kMagicInt + k into the code k + zero.
+struct KvGrid {
+    float scale, zero, inv_up, inv_dn;
+};
 
-// Eight codes (in the low bits of each q) packed, BITS == 4: one word; 8: two.
+// Eight codes (0 .. MAXQ) packed. BITS == 4: one word; 8: two.
 template <int BITS>
-__device__ __forceinline__ uint2 pack_codes(const uint32_t* q) {
+__device__ __forceinline__ uint2 pack_codes(const int* q) {
     if (BITS == 4)
-        return make_uint2(low_bytes((q[1] << 4) + (q[0] & 15u), (q[3] << 4) + (q[2] & 15u),
-                                    (q[5] << 4) + (q[4] & 15u), (q[7] << 4) + (q[6] & 15u)),
+        return make_uint2(((q[0] + (q[1] << 4)) + ((q[2] + (q[3] << 4)) << 8)) +
+                              (((q[4] + (q[5] << 4)) + ((q[6] + (q[7] << 4)) << 8)) << 16),
                           0);
-    return make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
+    return make_uint2((q[0] + (q[1] << 8)) + ((q[2] + (q[3] << 8)) << 16),
+                      (q[4] + (q[5] << 8)) + ((q[6] + (q[7] << 8)) << 16));
 }
 
 // The exact decision for all eight, out of line: few chunks need it.
 template <int BITS>
-__device__ __noinline__ uint2 kv_codes_exact(float4 a, float4 b, float scale, float zero, float inv) {
-    const QParams g{scale, zero, inv};
+__device__ __noinline__ uint2 kv_codes_exact(float4 a, float4 b, float scale, float zero) {
+    const QParams g{scale, zero, __frcp_rn(scale)};
     const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t q[8];
+    int q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(quant_code(v[i], g, (1 << BITS) - 1));
+    for (int i = 0; i < 8; ++i) q[i] = quant_code(v[i], g, (1 << BITS) - 1);
     return pack_codes<BITS>(q);
 }
 
-// Eight codes of one chunk. m = v * inv + magic holds the integer nearest to v * inv (one rounding).
-// inv is 1 / scale to 2^-24 and |v / scale| <= MAXQ, so the quotient is within (MAXQ + 1) * 2^-24 of
-// v * inv, and only where v * inv is nearer than 4 times that to a border is the exact decision
-// needed (one chunk in 4000 of 4 bits, in 500 of 8). The lower clamp is implied:
-// rint(lo/s) + rint(-lo/s) = 0.
+// Eight codes of one chunk. fma(v, inv, magic) holds the integer nearest to v * inv (one rounding).
+// With inv a factor 1 + 2^-22 and 1 - 2^-22 around the correctly rounded 1/scale, v * inv_up and
+// v * inv_dn enclose the exact quotient, so where both round to one integer the quotient does
+// too; where they differ (one chunk in about 4000 for 4 bits, 300 for 8) the exact decision is
+// made. The lower clamp is implied: rint(lo/s) + rint(-lo/s) = 0.
 template <int BITS>
-__device__ __forceinline__ uint2 kv_codes(const float* v, const QParams& g) {
+__device__ __forceinline__ uint2 kv_codes(const float* v, const KvGrid& g) {
     constexpr int MAXQ = (1 << BITS) - 1;
-    constexpr float kNear = 0.5f - (MAXQ + 1) * 0x1p-22f;
-    uint32_t q[8];
-    float far = 0.0f;
+    const int to_code = static_cast<int>(g.zero) - 0x4B400000;
+    int q[8];
+    uint32_t differ = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float m = fmaf(v[i], g.inv_scale, kMagicInt);
-        far = fmaxf(far, fabsf(fmaf(v[i], g.inv_scale, kMagicInt - m)));
-        q[i] = __float_as_uint(fminf(m + g.zero, kMagicInt + static_cast<float>(MAXQ)));
+        const int up = __float_as_int(fmaf(v[i], g.inv_up, kMagicInt));
+        const int dn = __float_as_int(fmaf(v[i], g.inv_dn, kMagicInt));
+        differ |= static_cast<uint32_t>(up ^ dn);
+        q[i] = __viaddmin_s32(up, to_code, MAXQ);
     }
-    if (far > kNear)
+    if (differ)
         return kv_codes_exact<BITS>(make_float4(v[0], v[1], v[2], v[3]),
-                                    make_float4(v[4], v[5], v[6], v[7]), g.scale, g.zero,
-                                    g.inv_scale);
+                                    make_float4(v[4], v[5], v[6], v[7]), g.scale, g.zero);
     return pack_codes<BITS>(q);
 }
+
+// A range {minimum, -maximum} of a chunk or group, so that one minimum joins both ends; NaN if any
+// value is. In the 16-bit types it is one packed register.
+template <typename T>
+struct KvRange;
+template <>
+struct KvRange<__half> {
+    __half2 r;
+    __device__ __forceinline__ void of(const uint4* x) {
+        __half2 a, b;
+        minmax_packed(x[0], a, b);
+        r = __halves2half2(__hmin_nan(__low2half(a), __high2half(a)),
+                           __hneg(__hmax_nan(__low2half(b), __high2half(b))));
+    }
+    __device__ __forceinline__ void join(int o) { r = __hmin2_nan(r, __shfl_xor_sync(0xffffffffu, r, o)); }
+    __device__ __forceinline__ KvRange from(int lane) const { return {__shfl_sync(0xffffffffu, r, lane)}; }
+    __device__ __forceinline__ float lo() const { return __low2float(r); }
+    __device__ __forceinline__ float hi() const { return -__high2float(r); }
+};
+template <>
+struct KvRange<__nv_bfloat16> {
+    __nv_bfloat162 r;
+    __device__ __forceinline__ void of(const uint4* x) {
+        __nv_bfloat162 a, b;
+        minmax_packed(x[0], a, b);
+        r = __halves2bfloat162(__hmin_nan(__low2bfloat16(a), __high2bfloat16(a)),
+                               __hneg(__hmax_nan(__low2bfloat16(b), __high2bfloat16(b))));
+    }
+    __device__ __forceinline__ void join(int o) { r = __hmin2_nan(r, __shfl_xor_sync(0xffffffffu, r, o)); }
+    __device__ __forceinline__ KvRange from(int lane) const { return {__shfl_sync(0xffffffffu, r, lane)}; }
+    __device__ __forceinline__ float lo() const { return __low2float(r); }
+    __device__ __forceinline__ float hi() const { return -__high2float(r); }
+};
+template <>
+struct KvRange<float> {
+    float mn, nmx;
+    __device__ __forceinline__ void of(const uint4* x) {
+        const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+        mn = __uint_as_float(w[0]);
+        nmx = -mn;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            mn = min_nan(mn, __uint_as_float(w[i]));
+            nmx = min_nan(nmx, -__uint_as_float(w[i]));
+        }
+    }
+    __device__ __forceinline__ void join(int o) {
+        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        nmx = min_nan(nmx, __shfl_xor_sync(0xffffffffu, nmx, o));
+    }
+    __device__ __forceinline__ KvRange from(int lane) const {
+        return {__shfl_sync(0xffffffffu, mn, lane), __shfl_sync(0xffffffffu, nmx, lane)};
+    }
+    __device__ __forceinline__ float lo() const { return mn; }
+    __device__ __forceinline__ float hi() const { return -nmx; }
+};
 
 // Quantise and write. The ranges of a warp's groups are found with shuffles by the TPG lanes of
 // each, but the groups' scalars (fp64, the dearest part: about 100 instructions) are computed by
@@ -137,49 +195,38 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
             if (slot >= 0 && slot < p.n_slots) dst = (is_v ? p.n_slots : 0) + slot;
             else if (slot >= 0) set_status(p.status, GPTQ_ERR_ARG);
         }
-        float mn[U], mx[U];
+        KvRange<T> range[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            vec_minmax(x[u][0], T(), mn[u], mx[u]);
-            if constexpr (VEC == 2) {
-                float a, b;
-                vec_minmax(x[u][1], T(), a, b);
-                mn[u] = min_nan(mn[u], a);
-                mx[u] = max_nan(mx[u], b);
-            }
+            range[u].of(x[u]);
 #pragma unroll
-            for (int o = TPG / 2; o > 0; o >>= 1) {
-                mn[u] = min_nan(mn[u], __shfl_xor_sync(0xffffffffu, mn[u], o));
-                mx[u] = max_nan(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], o));
-            }
+            for (int o = TPG / 2; o > 0; o >>= 1) range[u].join(o);
         }
 #pragma unroll
         for (int u0 = 0; u0 < U; u0 += UR) {
             // lane l computes the grid of pass u0 + l / GPP, group l % GPP
-            float lo = 0.0f, hi = 0.0f;
+            KvRange<T> mine = range[u0].from((lane % GPP) * TPG);
 #pragma unroll
-            for (int u = 0; u < UR; ++u) {
-                const float a = __shfl_sync(0xffffffffu, mn[u0 + u], (lane % GPP) * TPG);
-                const float b = __shfl_sync(0xffffffffu, mx[u0 + u], (lane % GPP) * TPG);
-                if (lane / GPP == u) {
-                    lo = a;
-                    hi = b;
-                }
+            for (int u = 1; u < UR; ++u) {
+                const KvRange<T> other = range[u0 + u].from((lane % GPP) * TPG);
+                if (lane / GPP == u) mine = other;
             }
+            const float lo = mine.lo(), hi = mine.hi();
             // (a difference with itself is 0 for finite values only)
             const bool finite = (lo - lo) == 0.0f && (hi - hi) == 0.0f;
-            QParams mine = group_params(finite ? lo : 0.0f, finite ? hi : 0.0f, MAXQ);
-            if (!finite || !(mine.scale <= 65504.0f)) {
-                mine.scale = __uint_as_float(0x7FC00000u);
-                mine.zero = 0.0f;
-            }
+            const QParams grid = group_params(finite ? lo : 0.0f, finite ? hi : 0.0f, MAXQ);
+            const bool usable = finite && grid.scale <= 65504.0f;
+            const float my_scale = usable ? grid.scale : __uint_as_float(0x7FC00000u);
+            const float my_zero = usable ? grid.zero : 0.0f;
 #pragma unroll
             for (int u = u0; u < u0 + UR; ++u) {
                 const int src = (u - u0) * GPP + lane / TPG;
-                QParams g;
-                g.scale = __shfl_sync(0xffffffffu, mine.scale, src);
-                g.zero = __shfl_sync(0xffffffffu, mine.zero, src);
-                g.inv_scale = __shfl_sync(0xffffffffu, mine.inv_scale, src);
+                const float inv = __shfl_sync(0xffffffffu, grid.inv_scale, src);
+                KvGrid g;
+                g.scale = __shfl_sync(0xffffffffu, my_scale, src);
+                g.zero = __shfl_sync(0xffffffffu, my_zero, src);
+                g.inv_up = inv * (1.0f + 0x1p-22f);
+                g.inv_dn = inv * (1.0f - 0x1p-22f);
                 if (dst < 0) continue;
                 const bool good = g.scale == g.scale;
                 float v[8];
@@ -343,6 +390,9 @@ static gptq_status kv_write_launch(const void* K, const void* V, int64_t n, int6
     if (p.wc % 128 == 0)
         return bits == 4 ? kv_write_group<T, 4, 4>(k, v, n, ks, vs, slots, p, s)
                          : kv_write_group<T, 8, 4>(k, v, n, ks, vs, slots, p, s);
+    if (p.wc % 64 == 0)
+        return bits == 4 ? kv_write_group<T, 4, 2>(k, v, n, ks, vs, slots, p, s)
+                         : kv_write_group<T, 8, 2>(k, v, n, ks, vs, slots, p, s);
     return bits == 4 ? kv_write_group<T, 4, 1>(k, v, n, ks, vs, slots, p, s)
                      : kv_write_group<T, 8, 1>(k, v, n, ks, vs, slots, p, s);
 }
@@ -361,9 +411,9 @@ static gptq_status kv_read_launch(const KvParams& p, int page_size, int64_t n_pa
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 64));
     T* k = static_cast<T*>(K);
     T* v = static_cast<T*>(V);
-    auto* kernel = p.wc % 128 == 0
-                       ? (bits == 4 ? kv_read_kernel<T, 4, 4> : kv_read_kernel<T, 8, 4>)
-                       : (bits == 4 ? kv_read_kernel<T, 4, 1> : kv_read_kernel<T, 8, 1>);
+    auto* kernel = p.wc % 128 == 0  ? (bits == 4 ? kv_read_kernel<T, 4, 4> : kv_read_kernel<T, 8, 4>)
+                   : p.wc % 64 == 0 ? (bits == 4 ? kv_read_kernel<T, 4, 2> : kv_read_kernel<T, 8, 2>)
+                                    : (bits == 4 ? kv_read_kernel<T, 4, 1> : kv_read_kernel<T, 8, 1>);
     GPTQ_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kKvThreads), 0, s, p, page_size, n_pages, table,
                              n_seqs, max_pages, cu, total, rows, k, v));
     GPTQ_LAUNCHED();

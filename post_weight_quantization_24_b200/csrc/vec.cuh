@@ -76,15 +76,11 @@ struct Vec<float> {
     static __device__ __forceinline__ float from_float(float x) { return x; }
 };
 
-// Minimum and maximum of a 16-byte vector's values; a NaN among them comes out as NaN.
+// Minima and maxima that carry a NaN along: the minimum of two fp32 values, both of
+// a 16-byte vector's packed pairs.
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 template <typename T2>
@@ -98,25 +94,6 @@ __device__ __forceinline__ void minmax_packed(const uint4& u, T2& mn, T2& mx) {
         mx = __hmax2_nan(mx, h);
     }
 }
-__device__ __forceinline__ void vec_minmax(const uint4& u, __half, float& mn, float& mx) {
-    __half2 a, b;
-    minmax_packed(u, a, b);
-    mn = min_nan(__low2float(a), __high2float(a));
-    mx = max_nan(__low2float(b), __high2float(b));
-}
-__device__ __forceinline__ void vec_minmax(const uint4& u, __nv_bfloat16, float& mn, float& mx) {
-    __nv_bfloat162 a, b;
-    minmax_packed(u, a, b);
-    mn = min_nan(__low2float(a), __high2float(a));
-    mx = max_nan(__low2float(b), __high2float(b));
-}
-__device__ __forceinline__ void vec_minmax(const uint4& u, float, float& mn, float& mx) {
-    const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                        __uint_as_float(u.w)};
-    mn = min_nan(min_nan(v[0], v[1]), min_nan(v[2], v[3]));
-    mx = max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3]));
-}
-
 // |x| as an unsigned integer: ordered like the magnitudes, infinity above every finite value
 // and NaN above infinity, so an integer maximum carries a NaN along.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
