@@ -499,13 +499,19 @@ def _float_code(dtype: torch.dtype, name: str) -> int:
     return code
 
 
-def _require(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=None) -> None:
-    """A contiguous tensor on the current CUDA device, of this type and shape."""
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    if dtype is not None and t.dtype != dtype:
+def _device() -> int:
+    """The current CUDA device; no tensor's (-2) before CUDA is in use, when all are the host's."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _require(t: torch.Tensor, name: str, dtype: torch.dtype | None = None, shape=None,
+             dev: int | None = None) -> None:
+    """A contiguous tensor on the current CUDA device (``dev``), of this type and shape."""
+    if dev is None:
+        dev = _device()
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on the current device")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -529,7 +535,7 @@ def fp8_quantize_act(X: torch.Tensor, out: tuple | None = None):
     code = _float_code(X.dtype, "X")
     nb = (d + 127) // 128
     if out is None:
-        codes = torch.empty(n, d, dtype=_E4M3, device=X.device)
+        codes = torch.empty_like(X, dtype=_E4M3)
         scales = torch.empty(nb, n, dtype=torch.float32, device=X.device)
     else:
         codes, scales = out
@@ -551,7 +557,7 @@ def fp8_quantize_weight(W: torch.Tensor, out: tuple | None = None):
     code = _float_code(W.dtype, "W")
     ns = ((d_out + 127) // 128, (d_in + 127) // 128)
     if out is None:
-        codes = torch.empty(d_out, d_in, dtype=_E4M3, device=W.device)
+        codes = torch.empty_like(W, dtype=_E4M3)
         scales = torch.empty(ns, dtype=torch.float32, device=W.device)
     else:
         codes, scales = out
@@ -568,23 +574,24 @@ def fp8_linear(X8: torch.Tensor, x_scales: torch.Tensor, W8: torch.Tensor,
                status: torch.Tensor | None = None) -> torch.Tensor:
     """Y = X̂·Ŵᵀ + R [n, d_out] (fp16/fp32/bf16) from fp8_quantize_act's and
     fp8_quantize_weight's codes and scales; R has Y's type and may be ``out``."""
-    _require(X8, "X8", _E4M3)
-    _require(W8, "W8", _E4M3)
+    dev = _device()
+    _require(X8, "X8", _E4M3, None, dev)
+    _require(W8, "W8", _E4M3, None, dev)
     if X8.dim() != 2 or W8.dim() != 2 or X8.shape[1] != W8.shape[1]:
         raise ValueError("X8 must be [n, d_in] and W8 [d_out, d_in]")
     n, d_in = X8.shape
     d_out = W8.shape[0]
     nb = (d_in + 127) // 128
-    _require(x_scales, "x_scales", torch.float32, (nb, n))
-    _require(w_scales, "w_scales", torch.float32, ((d_out + 127) // 128, nb))
+    _require(x_scales, "x_scales", torch.float32, (nb, n), dev)
+    _require(w_scales, "w_scales", torch.float32, ((d_out + 127) // 128, nb), dev)
     if out is None:
         code = _float_code(dtype, "dtype")
         out = torch.empty(n, d_out, dtype=dtype, device=X8.device)
     else:
-        _require(out, "out", None, (n, d_out))
+        _require(out, "out", None, (n, d_out), dev)
         code = _float_code(out.dtype, "out")
     if R is not None:
-        _require(R, "R", out.dtype, (n, d_out))
+        _require(R, "R", out.dtype, (n, d_out), dev)
     _require_status(status)
     _check(lib().fp8_linear(X8.data_ptr(), x_scales.data_ptr(), n, d_in, W8.data_ptr(),
                             w_scales.data_ptr(), d_out, _ptr(R), out.data_ptr(), code,
@@ -608,29 +615,29 @@ def kv_cache_alloc(n_pages: int, page_size: int, n_heads: int, head_dim: int, bi
     return codes, scales, torch.zeros_like(scales)
 
 
-def _cache_dims(codes, scales, zeros, bits):
+def _cache_dims(codes, scales, zeros, bits, dev):
     """(n_pages, page_size, n_heads, head_dim, group_size) of a cache's arrays, checked."""
-    _require(codes, "codes", torch.uint8)
-    if codes.dim() != 5 or codes.shape[0] != 2 or bits not in (4, 8) or codes.shape[4] < 1:
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != 5 or cs[0] != 2 or bits not in (4, 8) or cs[4] < 1:
         raise ValueError("codes must be [2, n_pages, page_size, n_heads, head_dim*bits/8], bits 4 or 8")
-    _, n_pages, page_size, n_heads, row = codes.shape
+    _, n_pages, page_size, n_heads, row = cs
     head_dim = row * 8 // bits
-    if scales.dim() != 5 or scales.shape[4] < 1 or head_dim % scales.shape[4]:
+    if len(ss) != 5 or ss[4] < 1 or head_dim % ss[4] or ss[:4] != cs[:4]:
         raise ValueError("scales must be [2, n_pages, page_size, n_heads, head_dim/group_size]")
-    shape = codes.shape[:4] + scales.shape[4:]
-    _require(scales, "scales", torch.float16, shape)
-    _require(zeros, "zeros", torch.float16, shape)
-    return n_pages, page_size, n_heads, head_dim, head_dim // scales.shape[4]
+    _require(codes, "codes", torch.uint8, None, dev)
+    _require(scales, "scales", torch.float16, None, dev)
+    _require(zeros, "zeros", torch.float16, ss, dev)
+    return n_pages, page_size, n_heads, head_dim, head_dim // ss[4]
 
 
-def _token_stride(t: torch.Tensor, name: str, n_heads: int, head_dim: int) -> int:
+def _token_stride(t: torch.Tensor, name: str, n_heads: int, head_dim: int, dev: int) -> int:
     """Elements from a token's row to the next; the row itself is contiguous."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.dim() != 3 or t.shape[1:] != (n_heads, head_dim):
         raise ValueError(f"{name} must be [n, {n_heads}, {head_dim}]")
     st = t.stride()
-    if t.numel() and (st[2] != 1 or (n_heads > 1 and st[1] != head_dim)):
+    if (st[2] != 1 or (n_heads > 1 and st[1] != head_dim)) and t.numel():
         raise ValueError(f"{name}: a token's heads must be contiguous")
     return st[0] if t.shape[0] > 1 else n_heads * head_dim
 
@@ -642,13 +649,14 @@ def kv_cache_write(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, codes:
     projection's output) into the cache's slots [n] int64 (page * page_size + place; negative:
     skipped; distinct). A slot behind the cache is skipped and sets ``status`` to
     GPTQ_ERR_ARG."""
-    n_pages, page_size, H, D, g = _cache_dims(codes, scales, zeros, bits)
-    ks, vs = _token_stride(K, "K", H, D), _token_stride(V, "V", H, D)
+    dev = _device()
+    n_pages, page_size, H, D, g = _cache_dims(codes, scales, zeros, bits, dev)
+    ks, vs = _token_stride(K, "K", H, D, dev), _token_stride(V, "V", H, D, dev)
     code = _float_code(K.dtype, "K")
-    if V.dtype != K.dtype or V.shape != K.shape:
-        raise ValueError("V must have K's type and shape")
     n = K.shape[0]
-    _require(slots, "slots", torch.int64, (n,))
+    if V.dtype is not K.dtype or V.shape[0] != n:
+        raise ValueError("V must have K's type and shape")
+    _require(slots, "slots", torch.int64, (n,), dev)
     _require_status(status)
     _check(lib().kv_cache_write(K.data_ptr(), V.data_ptr(), code, n, ks, vs, H, D,
                                 slots.data_ptr(), n_pages * page_size, bits, g, codes.data_ptr(),
@@ -664,16 +672,17 @@ def kv_cache_read(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
     0 .. len-1 of each sequence in turn. page_table int32 [n_seqs, max_pages], cu_lens int32
     [n_seqs + 1] (running sums of the lengths). Rows behind cu_lens[-1] are left as they were;
     positions without a page of the cache come as zeros and set ``status`` to GPTQ_ERR_ARG."""
-    n_pages, page_size, H, D, g = _cache_dims(codes, scales, zeros, bits)
-    _require(page_table, "page_table", torch.int32)
+    dev = _device()
+    n_pages, page_size, H, D, g = _cache_dims(codes, scales, zeros, bits, dev)
+    _require(page_table, "page_table", torch.int32, None, dev)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n_seqs, max_pages]")
     n_seqs, max_pages = page_table.shape
-    _require(cu_lens, "cu_lens", torch.int32, (n_seqs + 1,))
+    _require(cu_lens, "cu_lens", torch.int32, (n_seqs + 1,), dev)
     if out is None:
         code = _float_code(dtype, "dtype")
         K = torch.empty(total, H, D, dtype=dtype, device=codes.device)
-        V = torch.empty(total, H, D, dtype=dtype, device=codes.device)
+        V = torch.empty_like(K)
     else:
         K, V = out
         code = _float_code(K.dtype, "K")
