@@ -13,6 +13,10 @@ addition are off by 2^-24 each, relative to Σ|x̂·ŵ| (+ |R|). One rounding to
 half a step.
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -149,6 +153,52 @@ def test_linear_on_large_layers(cuda_lib, n, d_in, d_out):
     _check_linear(cuda_lib, n, d_in, d_out, F16, True, seed=n)
 
 
+@pytest.mark.parametrize("n,d_in,d_out,dtype,res", [
+    (1030, 272, 2056, F16, True),         # ragged in tokens, channels and input channels
+    (1030, 128, 2049, BF16, True),        # odd rows of Y
+    (770, 400, 3300, F32, True),          # fp32 rows leave in two rounds
+    (2600, 144, 4104, F16, False),        # several tiles per pair of SMs
+    (2600, 144, 4104, BF16, True),
+    (2600, 16, 4100, F32, True),
+    (5000, 256, 1030, F16, False),
+])
+def test_linear_with_many_tiles(cuda_lib, n, d_in, d_out, dtype, res):
+    """Calls with enough 256 x 256 tiles for pairs of SMs, the residual in place and not."""
+    dev, Y = _check_linear(cuda_lib, n, d_in, d_out, dtype, res, seed=n)
+    if res:
+        R = _values(n, d_out, n + 2, dtype=dtype, spread=0.0).cuda()
+        assert cuda_lib.fp8_linear(*dev, R=R, out=R) is R and torch.equal(R, Y)
+    else:
+        assert torch.equal(cuda_lib.fp8_linear(*dev, dtype=dtype), Y)
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """More than 2^31 elements of X, its codes and Y: the last rows are right."""
+    n, d = 66000, 33024
+    x = torch.empty(n, d, dtype=F16, device="cuda")
+    tail = _values(3, d, seed=1)
+    x[-3:] = tail.cuda()
+    x[:-3] = 1.0
+    codes, scales = cuda_lib.fp8_quantize_act(x)
+    rc, rs = ofp8.quantize_act(_np(tail))
+    _same(_np(codes[-3:]), rc)
+    _same(_np(scales[:, -3:]), rs.astype(np.float64))
+    wcodes, _ = cuda_lib.fp8_quantize_weight(x)
+    assert bool((wcodes[:256].float() == 448).all())
+    last = (n - 1) // 128 * 128
+    rc, _ = ofp8.quantize_weight(_np(x[last:]))
+    _same(_np(wcodes[last:]), rc)
+    del x, codes, wcodes
+    host, dev = _quantized(4, 16, d, seed=2)
+    x8 = dev[0].repeat(n // 4, 1)
+    sx = dev[1].repeat(1, n // 4)
+    Y = cuda_lib.fp8_linear(x8, sx, dev[2], dev[3])
+    assert Y.numel() > 1 << 31
+    ref, mag = ofp8.linear(*host)
+    assert np.all(np.abs(_np(Y[-4:]) - ref) <= _tolerance(mag, ref, None, 16, F16))
+    assert torch.equal(Y[:4], Y[-4:])
+
+
 @pytest.mark.parametrize("n", [1, 7, 12, 40, 90, 150, 600])
 @pytest.mark.parametrize("d_in,d_out", [(272, 136), (1024, 1296)])
 def test_linear_is_exact_on_small_integers(cuda_lib, n, d_in, d_out):
@@ -181,11 +231,11 @@ def test_linear_residual_in_place_and_rows_around_it(cuda_lib, n):
     assert torch.equal(buf[0], before[0]) and torch.equal(buf[-1], before[-1])
 
 
-@pytest.mark.parametrize("n", [3, 20, 150])
-def test_linear_keeps_nan_to_its_token_and_channels(cuda_lib, n):
+@pytest.mark.parametrize("n,d_out", [(3, 300), (20, 300), (150, 300), (2000, 2600)])
+def test_linear_keeps_nan_to_its_token_and_channels(cuda_lib, n, d_out):
     """A token with a NaN block gives a NaN row; a weight block with NaN codes and scale gives NaN
     columns; nothing else changes."""
-    host, dev = _quantized(n, 256, 300, seed=1)
+    host, dev = _quantized(n, 256, d_out, seed=1)
     clean = cuda_lib.fp8_linear(*dev)
     x8, sx, w8, sw = [t.clone() for t in dev]
     x8.view(torch.uint8)[1, 128:] = 0x7F
@@ -193,18 +243,18 @@ def test_linear_keeps_nan_to_its_token_and_channels(cuda_lib, n):
     w8.view(torch.uint8)[128:256, :128] = 0x7F
     sw[1, 0] = float("nan")
     Y = cuda_lib.fp8_linear(x8, sx, w8, sw)
-    bad = torch.zeros(n, 300, dtype=torch.bool, device="cuda")
+    bad = torch.zeros(n, d_out, dtype=torch.bool, device="cuda")
     bad[1] = True
     bad[:, 128:256] = True
     assert torch.equal(torch.isnan(Y), bad)
     assert torch.equal(Y[~bad], clean[~bad])
 
 
-@pytest.mark.parametrize("n", [1, 33, 100, 700])
-def test_linear_repeats_its_bits_and_runs_from_a_graph(cuda_lib, n):
+@pytest.mark.parametrize("n,d_out", [(1, 520), (33, 520), (100, 520), (700, 520), (1300, 2304)])
+def test_linear_repeats_its_bits_and_runs_from_a_graph(cuda_lib, n, d_out):
     """Equal inputs give equal bits; a captured call replays on new inputs, also while another
     call runs on another stream."""
-    d_in, d_out = 2064, 520
+    d_in = 2064
     _, dev = _quantized(n, d_in, d_out, seed=3)
     _, dev2 = _quantized(n, d_in, d_out, seed=30)
     want = [cuda_lib.fp8_linear(*d, dtype=F32) for d in (dev, dev2)]
@@ -227,6 +277,45 @@ def test_linear_repeats_its_bits_and_runs_from_a_graph(cuda_lib, n):
     torch.cuda.synchronize()
     assert torch.equal(out, want[1])
     assert all(torch.equal(s, want[0]) for s in side)
+
+
+_CAPTURE_FIRST = """
+import torch
+from post_weight_quantization_24_b200 import gptq
+x = torch.randn(200, 256, device='cuda').half()
+cache = gptq.kv_cache_alloc(40, 16, 2, 64, 8, 64)
+slots = torch.arange(200, device='cuda')
+table = torch.arange(13, dtype=torch.int32, device='cuda').view(1, 13)
+cu = torch.tensor([0, 200], dtype=torch.int32, device='cuda')
+def run():
+    w8, sw = gptq.fp8_quantize_weight(x)
+    out = []
+    for n in (1, 30, 60, 120, 200):
+        out.append(gptq.fp8_linear(*gptq.fp8_quantize_act(x[:n]), w8, sw))
+    big = x.repeat(8, 1)
+    out.append(gptq.fp8_linear(*gptq.fp8_quantize_act(big), *gptq.fp8_quantize_weight(big)))
+    kv = x[:, :128].unflatten(1, (2, 64))
+    gptq.kv_cache_write(kv, kv, slots, *cache)
+    return out + list(gptq.kv_cache_read(*cache, table, cu, 200))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    captured = run()
+g.replay()
+torch.cuda.synchronize()
+again = run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, again))
+print('captured')
+"""
+
+
+def test_first_calls_may_be_captured(cuda_lib):
+    """A process whose first calls are inside a capture: no warm-up is needed."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _CAPTURE_FIRST], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_empty_calls(cuda_lib):
