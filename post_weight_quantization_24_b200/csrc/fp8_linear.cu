@@ -692,12 +692,16 @@ static gptq_status f8_launch(void (*kernel)(KArgs...), int grid, int cluster, in
     return GPTQ_OK;
 }
 
-// Ways to split the input channels of `tiles` streaming tiles: as many as fit the GPU at once (where
-// two CTAs share an SM, the last doubling may go past one per SM).
+// Ways to split the input channels of `tiles` streaming tiles, a power of two up to 8: until there is
+// a CTA for every SM, as long as each keeps 2 blocks (1 token, 1024 -> 1024: 4.6 us in quarters,
+// 4.9 us in halves). Where two CTAs share an SM, one more doubling pays if each keeps 8 blocks (37
+// tokens, 11008 -> 4096: 15.5 us in eighths, 17.1 us in quarters), and costs with fewer (64 tokens,
+// 4096 -> 4096: 11.3 us in eighths, 9.7 us in quarters).
 static int f8_splits(long long tiles, int n_kb, int per_sm) {
     int splits = 1;
-    while (splits < 8 && 2 * splits <= n_kb &&
-           (per_sm == 2 ? tiles * splits < num_sms() : 2 * tiles * splits <= num_sms()))
+    while (splits < 8 &&
+           ((2 * tiles * splits <= num_sms() && 4 * splits <= n_kb) ||
+            (per_sm == 2 && tiles * splits < num_sms() && 16 * splits <= n_kb)))
         splits *= 2;
     return splits;
 }
