@@ -297,14 +297,22 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
         for (int i = warp - 3; i < share; i += C::EPI_WARPS) {
             const int t = rank * share + i, row = t0 + t;
             if (row >= p.n_tok || col >= p.d_out) continue;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int r = 0; r < splits; ++r) {
-                const float4 x = ld_cluster_f4(
-                    mapa_shared(mine + static_cast<uint32_t>(t * f8s::BM * 4), static_cast<uint32_t>(r)));
-                v[0] += x.x;
-                v[1] += x.y;
-                v[2] += x.z;
-                v[3] += x.w;
+            // all ranks' sums are asked for before the first is added: one trip across the cluster
+            float4 x[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < splits)
+                    x[r] = ld_cluster_f4(mapa_shared(mine + static_cast<uint32_t>(t * f8s::BM * 4),
+                                                     static_cast<uint32_t>(r)));
+            float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+#pragma unroll
+            for (int r = 1; r < 8; ++r) {
+                if (r < splits) {
+                    v[0] += x[r].x;
+                    v[1] += x[r].y;
+                    v[2] += x[r].z;
+                    v[3] += x[r].w;
+                }
             }
             const int64_t off = static_cast<int64_t>(row) * p.d_out + col;
             const T* R = p.R ? static_cast<const T*>(p.R) + off : nullptr;
