@@ -421,7 +421,9 @@ gptq_status fp8_quantize_weight(const void* W, int w_dtype, int d_out, int d_in,
  *   Y        device [n_tokens x d_out], fp16, fp32 or bf16 (y_dtype).
  *            X8, W8, Y and R 16-byte aligned.
  *   status_dev device int or NULL: set to GPTQ_ERR_TIMEOUT if a bounded wait gave up.
- * Asynchronous; equal inputs give equal bits. Errors: ARG, CUDA, UNSUPPORTED. */
+ * Y may overlap no other argument but R. The order in which blocks are summed depends on the
+ * sizes (n_tokens among them). Asynchronous, no workspace, may be captured; equal inputs give equal
+ * bits. Errors: ARG, CUDA, UNSUPPORTED. */
 gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int64_t n_tokens, int d_in,
                        const uint8_t* W8, const float* w_scales, int d_out, const void* R, void* Y,
                        int y_dtype, int* status_dev, void* stream);
@@ -445,8 +447,8 @@ gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int64_t n_token
 
 /* Quantise and write n_tokens tokens.
  *   K, V     device, fp16, fp32 or bf16: token t's [n_heads x head_dim] keys start at element
- *            t * k_stride, its values at t * v_stride (strides >= 0, multiples of 16 bytes: views
- *            of a fused projection's output need no copy). 16-byte aligned.
+ *            t * k_stride, its values at t * v_stride (strides 0 .. 2^31, multiples of 16 bytes:
+ *            views of a fused projection's output need no copy). 16-byte aligned.
  *   slots    device int64 [n_tokens]: each token's slot. A negative slot skips the token. Slots of
  *            one call must be distinct: a slot given twice ends with unspecified contents (no
  *            other slot is touched).

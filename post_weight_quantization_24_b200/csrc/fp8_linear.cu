@@ -10,9 +10,14 @@
 // kernel records GPTQ_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns. Tokens and
 // channels past the edges are zero-filled by TMA and not stored.
 //   fp8_pair_kernel    256 tokens x 256 channels per CTA pair, for calls with enough such tiles to
-//                      fill the GPU: bound by the tensor cores and, over long runs, by power;
+//                      fill the GPU. 16384 tokens, 11008 -> 4096, fp16 with residual: 0.75 to 0.81
+//                      ms (1.8 to 2.0 PFLOP/s), 0.85 ms in long runs at the power limit, where
+//                      TMA and MMAs alone take 0.61 ms; without the promotion's multiply-adds
+//                      0.71 ms.
 //   fp8_stream_kernel  128 channels x 16 to 128 tokens per CTA, the input channels split over a
-//                      cluster: for all other calls, bound by streaming the weights.
+//                      cluster: for all other calls. 1 token, 4096 -> 4096: 7.2 us; 37 tokens,
+//                      11008 -> 4096, bf16 with residual: 15.5 us, about 5 us of them fixed
+//                      (set-up, first loads, the join) and the rest at 4 to 5 TB/s of weights.
 #include <algorithm>
 #include <atomic>
 
@@ -33,38 +38,21 @@ struct F8Params {
     int* status;
 };
 
-// NC accumulated columns of one row -> Y (+ R), columns col0 .. min(col0 + NC, d_out)
+// NC accumulated columns of one row -> Y (+ R), value by value: for rows that do not all start on
+// 16-byte boundaries.
 template <typename T, int NC>
 __device__ __forceinline__ void f8_store(const F8Params& p, int row, int col0,
                                          const uint64_t (&acc)[NC / 2]) {
-    constexpr int N = Vec<T>::N;
-    if (row >= p.n_tok || col0 >= p.d_out) return;
+    if (row >= p.n_tok) return;
     const int64_t off = static_cast<int64_t>(row) * p.d_out + col0;
     T* y = static_cast<T*>(p.Y) + off;
     const T* r = p.R ? static_cast<const T*>(p.R) + off : nullptr;
     const int left = p.d_out - col0;
-    if (p.vec_ok) {       // d_out is a multiple of N
 #pragma unroll
-        for (int c = 0; c < NC; c += N) {
-            if (c >= left) break;
-            float v[N];
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = f32x2_get(acc[(c + e) / 2], e & 1);
-            if (r) {
-                float f[N];
-                Vec<T>::unpack(*reinterpret_cast<const uint4*>(r + c), f);
-#pragma unroll
-                for (int e = 0; e < N; ++e) v[e] += f[e];
-            }
-            *reinterpret_cast<uint4*>(y + c) = Vec<T>::pack(v);
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (c < left)
-                y[c] = Vec<T>::from_float(f32x2_get(acc[c / 2], c & 1) +
-                                          (r ? Vec<T>::to_float(r[c]) : 0.0f));
-        }
+    for (int c = 0; c < NC; ++c) {
+        if (c < left)
+            y[c] = Vec<T>::from_float(f32x2_get(acc[c / 2], c & 1) +
+                                      (r ? Vec<T>::to_float(r[c]) : 0.0f));
     }
 }
 
@@ -90,7 +78,10 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, int
 // that a few tokens cost a narrow N instead of an M of 128 rows. A cluster of S CTAs splits the
 // tile's input channels; each CTA streams its part of the weights (16 KB per block through a
 // ring of stages), and the S partial sums are added over distributed shared memory in rank order,
-// so equal inputs give equal bits. One CTA's ring keeps about 100 KB in flight, and two fit an SM.
+// so equal inputs give equal bits. One CTA's ring keeps about 100 KB in flight, and two fit an SM
+// (one of 192 KB for 128 tokens: 128 tokens, 11008 -> 4096, took 24 us with one, 31 us with two of
+// 96 KB).
+// With tokens as M and no split the 37-token call above took 43.6 us.
 //   warp 0    TMA producer            warps 1, 2  MMA issuers, every other block each
 //   warps 3-  promotion: a thread owns one channel and EC tokens. The factors sx*sw (one per token
 //             and block) are put into shared memory for FBLK blocks at a time, which exposes
@@ -112,6 +103,10 @@ struct Cfg {
     static constexpr uint32_t IDESC = umma_idesc_e4m3(BM, NT);
     static_assert(NT * BM * 4 <= STAGES * STAGE, "the partial sums reuse the ring");
     static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024, "CTAs per SM");
+    // An issuer waits for its accumulator first: that block it - ACCS has been added tells that the
+    // stage's last load (block it - STAGES) landed, so a parity wait on the stage cannot take the
+    // phase before last for the last. An accumulator belongs to one issuer for the same reason.
+    static_assert(ACCS % 2 == 0 && STAGES >= ACCS, "phases in order");
 };
 }  // namespace f8s
 
@@ -441,14 +436,13 @@ __device__ __forceinline__ bool f8_store_boxes(const CUtensorMap* ymap, const CU
 
 // Tiles run in bands of 8 token tiles with the token tile varying fastest, so the CTAs that run
 // together share weight tiles and activation rows in L2.
-__device__ __forceinline__ void f8_tile(const F8Params& p, int t, int bm, int bn, int& m0,
-                                        int& n0) {
+__device__ __forceinline__ void f8_tile(const F8Params& p, int t, int& m0, int& n0) {
     const int per_band = f8p::BAND * p.n_nt;
     const int band = t / per_band;
     const int rem = t - band * per_band;
     const int band_m = min(f8p::BAND, p.n_mt - band * f8p::BAND);
-    m0 = (band * f8p::BAND + rem % band_m) * bm;
-    n0 = (rem / band_m) * bn;
+    m0 = (band * f8p::BAND + rem % band_m) * f8p::PT;
+    n0 = (rem / band_m) * f8p::PT;
 }
 
 template <typename T>
@@ -507,7 +501,7 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
             int it = 0;
             for (int t = cluster; t < p.n_tiles && !*abort_flag; t += n_clusters) {
                 int m0, n0;
-                f8_tile(p, t, f8p::PT, f8p::PT, m0, n0);
+                f8_tile(p, t, m0, n0);
                 m0 += f8p::BM * static_cast<int>(rank);
                 n0 += f8p::BNC * static_cast<int>(rank);
                 for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
@@ -591,7 +585,7 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
         bool stop = false;
         for (int t = cluster; t < p.n_tiles && !stop; t += n_clusters) {
             int m0, n0;
-            f8_tile(p, t, f8p::PT, f8p::PT, m0, n0);
+            f8_tile(p, t, m0, n0);
             const int col0 = n0 + f8p::HN * h;
             if (boxes && res && lane == 0) {
                 bulk_wait_read<0>();                 // the last tile has left the boxes

@@ -8,7 +8,9 @@
 // gets s = r = NaN and NaN codes.
 //
 // Both kernels read X once into registers and write its codes from there: bytes per value are
-// the input's 2 or 4 plus 1, plus the scales. They are bound by HBM.
+// the input's 2 or 4 plus 1, plus the scales. They are bound by HBM: 16384 x 11008 bf16 activations
+// take 93 us (5.9 TB/s), 11008 x 4096 fp16 weights 21 us (6.3 TB/s), 4100 x 5136 fp32 weights 17
+// us (6.1 TB/s); a copy runs at 6.55 TB/s.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -63,7 +65,8 @@ __device__ __forceinline__ uint32_t amax_vec(const uint4& u, uint32_t m) {
 // A CTA takes 8 tokens x 1024 channels. A warp takes one token: 8 lanes per 128-channel block, 4
 // blocks per pass, 2 passes, all loads first; a lane's vectors lie 8 vectors apart, so that every
 // load and store of 8 lanes is one contiguous run (a pass of fp16 is 1 KB of one row). The scales
-// leave through shared memory as runs of 8 tokens.
+// leave through shared memory as runs of 8 tokens. (With 4 tokens x 128 channels per warp, 256 bytes
+// of a row at a time, and plain loads it took 101 us instead of 93.)
 template <typename T>
 __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, int64_t n, int d,
                                                       uint8_t* __restrict__ codes,
@@ -111,7 +114,9 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
     }
 }
 
-// A block of 256 threads takes one 128 x 128 block: 8 lanes per row, 4 rows per warp and step.
+// A CTA of 256 threads takes one 128 x 128 block, all of it in flight at once (32 KB of fp16): 8
+// lanes per row, 4 rows per warp and step. Registers are bounded for three CTAs per SM with 16-bit
+// inputs (with that, streaming loads and the overlapped launch 26.5 us became 21).
 template <typename T>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp8_weight_kernel(const T* __restrict__ W, int d_out,
                                                          int d_in, uint8_t* __restrict__ codes,
