@@ -15,8 +15,8 @@
 //                      TMA and MMAs alone take 0.61 ms; without the promotion's multiply-adds
 //                      0.71 ms.
 //   fp8_stream_kernel  128 channels x 16 to 128 tokens per CTA, the input channels split over a
-//                      cluster: for all other calls. 1 token, 4096 -> 4096: 7.2 us; 37 tokens,
-//                      11008 -> 4096, bf16 with residual: 15.5 us, about 5 us of them fixed
+//                      cluster: for all other calls. 1 token, 4096 -> 4096: 7.4 us; 37 tokens,
+//                      11008 -> 4096, bf16 with residual: 15.2 us, 4 to 5 us of them fixed
 //                      (set-up, first loads, the join) and the rest at 4 to 5 TB/s of weights.
 #include <algorithm>
 #include <atomic>
@@ -77,8 +77,11 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, int
 // Streaming kernel: Y^T tiles of 128 channels x NT tokens, the weights as the MMA's M operand, so
 // that a few tokens cost a narrow N instead of an M of 128 rows. A cluster of S CTAs splits the
 // tile's input channels; each CTA streams its part of the weights (16 KB per block through a
-// ring of stages), and the S partial sums are added over distributed shared memory in rank order,
-// so equal inputs give equal bits. One CTA's ring keeps about 100 KB in flight, and two fit an SM
+// ring of stages), and sends its partial sums to the CTAs that own their tokens (st.async into their
+// shared memory, counted on an mbarrier there), which add them in rank order, so equal inputs
+// give equal bits. Nobody reads another CTA's memory, so no cluster barrier (1100 cycles each) is
+// left but one whose latency the main loop covers (read instead of sent, with
+// a barrier before and after: 16 tokens, 11008 -> 4096, 12.9 us against 11.7). One CTA's ring keeps about 100 KB in flight, and two fit an SM
 // (one of 192 KB for 128 tokens: 128 tokens, 11008 -> 4096, took 24 us with one, 31 us with two of
 // 96 KB).
 // With tokens as M and no split the 37-token call above took 43.6 us.
@@ -92,16 +95,16 @@ constexpr int BM = 128, BK = 128;
 template <int NT>
 struct Cfg {
     static constexpr int PER_SM = NT == 128 ? 1 : 2;              // CTAs that fit an SM
-    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 6;
+    static constexpr int STAGES = NT == 16 ? 5 : NT == 32 ? 4 : NT == 64 ? 3 : 4;
     static constexpr int A_BYTES = BM * BK, STAGE = A_BYTES + NT * BK;
-    static constexpr int ACCS = NT == 128 ? 2 : 4;
+    static constexpr int ACCS = NT >= 64 ? 2 : 4;
     static constexpr uint32_t TMEM_COLS = ACCS * NT;
     static constexpr int EC = NT <= 32 ? 16 : 32, EPI_WARPS = 4 * (NT / EC);
     static constexpr int EPI_THREADS = EPI_WARPS * 32, THREADS = 96 + EPI_THREADS;
-    static constexpr int FBLK = NT == 128 ? 16 : 32;             // blocks of factors kept
-    static constexpr int SMEM = 1024 + STAGES * STAGE + FBLK * NT * 4 + 256;
+    static constexpr int FBLK = NT >= 64 ? 16 : 32;              // blocks of factors kept
+    static constexpr int RECV = NT * BM * 4;                     // the cluster's sums of this CTA's tokens
+    static constexpr int SMEM = 1024 + STAGES * STAGE + RECV + FBLK * NT * 4 + 256;
     static constexpr uint32_t IDESC = umma_idesc_e4m3(BM, NT);
-    static_assert(NT * BM * 4 <= STAGES * STAGE, "the partial sums reuse the ring");
     static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024, "CTAs per SM");
     // An issuer waits for its accumulator first: that block it - ACCS has been added tells that the
     // stage's last load (block it - STAGES) landed, so a parity wait on the stage cannot take the
@@ -109,14 +112,6 @@ struct Cfg {
     static_assert(ACCS % 2 == 0 && STAGES >= ACCS, "phases in order");
 };
 }  // namespace f8s
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(cluster_addr));
-    return v;
-}
 
 template <typename T, int NT>
 __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
@@ -126,13 +121,15 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float* factors = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);      // [FBLK][NT]
+    float* recv = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);         // [rank][token][channel]
+    float* factors = recv + C::RECV / 4;                                         // [FBLK][NT]
     uint64_t* full = reinterpret_cast<uint64_t*>(factors + C::FBLK * NT);
     uint64_t* empty = full + C::STAGES;
     uint64_t* acc_full = empty + C::STAGES;
     uint64_t* acc_empty = acc_full + C::ACCS;
     uint64_t* drained = acc_empty + C::ACCS;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
+    uint64_t* recv_full = drained + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(recv_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = warp_id(), lane = lane_id();
@@ -152,10 +149,24 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
         }
         mbar_init(&drained[0], 1);
         mbar_init(&drained[1], 1);
+        mbar_init(recv_full, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&xmap);
-        tma_prefetch_desc(&wmap);
+        mbar_arrive_expect_tx(recv_full, C::RECV);
+    }
+    auto load = [&](int it) {      // block it of this CTA into its stage
+        const int st = it % C::STAGES;
+        uint8_t* sa = smem + st * C::STAGE;
+        const int x = (kb0 + it) * f8s::BK;
+        mbar_arrive_expect_tx(&full[st], C::STAGE);
+        tma_load_2d(sa, &wmap, &full[st], x, c0);
+        tma_load_2d(sa + C::A_BYTES, &xmap, &full[st], x, t0);
+    };
+    const int first = min(C::STAGES, n_kb);
+    if (threadIdx.x == 0) {
+        // the first loads leave while the rest is still being set up
+        pdl_wait();
+        for (int it = 0; it < first; ++it) load(it);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -164,24 +175,20 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    cluster_arrive();   // this CTA's barriers exist; waited for before anything is sent
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();         // nothing the previous kernel may have written was read so far
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            int it = first;
             for (; it < n_kb && !*abort_flag; ++it) {
-                const int st = it % C::STAGES;
-                if (!mbar_wait(&empty[st], ((it / C::STAGES) & 1) ^ 1)) {
+                if (!mbar_wait(&empty[it % C::STAGES], ((it / C::STAGES) & 1) ^ 1)) {
                     set_status(p.status, GPTQ_ERR_TIMEOUT);
                     *abort_flag = 1;
                     break;
                 }
-                uint8_t* sa = smem + st * C::STAGE;
-                const int x = (kb0 + it) * f8s::BK;
-                mbar_arrive_expect_tx(&full[st], C::STAGE);
-                tma_load_2d(sa, &wmap, &full[st], x, c0);
-                tma_load_2d(sa + C::A_BYTES, &xmap, &full[st], x, t0);
+                load(it);
             }
             const int n_tail = it < C::STAGES ? it : C::STAGES;
             for (int k = it - n_tail; k < it; ++k) {
@@ -274,40 +281,34 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
                 }
             }
         }
-        // the ring is free: the last block's MMAs have read their stage. Partial sums [token][channel]
-        float* red = reinterpret_cast<float*>(smem);
+        // every token's sums to the CTA that owns it, as [rank][token of the owner][channel]
+        const int share = NT / splits, shift = 31 - __clz(share);
+        const uint32_t my_part = smem_u32(recv) +
+                                 static_cast<uint32_t>((rank * share * f8s::BM + 32 * q + lane) * 4);
+        __syncwarp();
+        cluster_wait();
 #pragma unroll
-        for (int k = 0; k < C::EC; ++k) red[(g * C::EC + k) * f8s::BM + 32 * q + lane] = acc[k];
-    }
-
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
-    cluster_sync();     // every CTA's partial sums are in its shared memory
-    if (warp >= 3) {
+        for (int k = 0; k < C::EC; ++k) {
+            const int t = g * C::EC + k, owner = t >> shift;
+            st_async_b32(mapa_shared(my_part + static_cast<uint32_t>((t & (share - 1)) * f8s::BM * 4),
+                                     static_cast<uint32_t>(owner)),
+                         __float_as_uint(acc[k]),
+                         mapa_shared(smem_u32(recv_full), static_cast<uint32_t>(owner)));
+        }
         // this CTA's share of the tokens: a warp takes a token, a lane four channels
-        const int share = NT / splits, col = c0 + 4 * lane;
-        const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(16 * lane);
+        const bool got = f8_warp_wait(recv_full, 0, p.status, abort_flag);
+        const int col = c0 + 4 * lane;
         for (int i = warp - 3; i < share; i += C::EPI_WARPS) {
-            const int t = rank * share + i, row = t0 + t;
-            if (row >= p.n_tok || col >= p.d_out) continue;
-            // all ranks' sums are asked for before the first is added: one trip across the cluster
-            float4 x[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < splits)
-                    x[r] = ld_cluster_f4(mapa_shared(mine + static_cast<uint32_t>(t * f8s::BM * 4),
-                                                     static_cast<uint32_t>(r)));
-            float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
-#pragma unroll
-            for (int r = 1; r < 8; ++r) {
-                if (r < splits) {
-                    v[0] += x[r].x;
-                    v[1] += x[r].y;
-                    v[2] += x[r].z;
-                    v[3] += x[r].w;
-                }
+            const int row = t0 + rank * share + i;
+            if (!got || row >= p.n_tok || col >= p.d_out) continue;
+            const float4* x = reinterpret_cast<const float4*>(recv + i * f8s::BM) + lane;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < splits; ++r) {
+                const float4 y4 = x[r * share * (f8s::BM / 4)];
+                v[0] += y4.x;
+                v[1] += y4.y;
+                v[2] += y4.z;
+                v[3] += y4.w;
             }
             const int64_t off = static_cast<int64_t>(row) * p.d_out + col;
             const T* R = p.R ? static_cast<const T*>(p.R) + off : nullptr;
@@ -331,8 +332,25 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
             }
         }
     }
-    __syncwarp();
-    cluster_sync();     // no CTA leaves while another may still read its sums
+    if (warp < 3) {
+        __syncwarp();
+        cluster_wait();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+    if (*abort_flag) {
+        // sums for this CTA may still be under way: it stays until the others have left (they need
+        // nothing of it) or wait here too
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // ---------------------------------------------------------------------------------------
