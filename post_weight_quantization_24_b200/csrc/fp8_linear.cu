@@ -76,15 +76,14 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, int
 // ---------------------------------------------------------------------------------------
 // Streaming kernel: Y^T tiles of 128 channels x NT tokens, the weights as the MMA's M operand, so
 // that a few tokens cost a narrow N instead of an M of 128 rows. A cluster of S CTAs splits the
-// tile's input channels; each CTA streams its part of the weights (16 KB per block through a
-// ring of stages), and sends its partial sums to the CTAs that own their tokens (st.async into their
-// shared memory, counted on an mbarrier there), which add them in rank order, so equal inputs
-// give equal bits. Nobody reads another CTA's memory, so no cluster barrier (1100 cycles each) is
-// left but one whose latency the main loop covers (read instead of sent, with
-// a barrier before and after: 16 tokens, 11008 -> 4096, 12.9 us against 11.7). One CTA's ring keeps about 100 KB in flight, and two fit an SM
-// (one of 192 KB for 128 tokens: 128 tokens, 11008 -> 4096, took 24 us with one, 31 us with two of
-// 96 KB).
-// With tokens as M and no split the 37-token call above took 43.6 us.
+// tile's input channels. Each CTA streams its part of the weights (16 KB per block) through a ring of
+// stages and sends its partial sums to the CTAs that own their tokens (st.async into their shared
+// memory, counted on an mbarrier there), which add them in rank order, so equal inputs give equal
+// bits. Nobody reads another CTA's memory, so no cluster barrier (1100 cycles each) is left but
+// one whose latency the main loop covers: 16 tokens, 11008 -> 4096, 11.7 us against 12.9 with sums
+// read between two barriers. Two CTAs fit an SM, one for 128 tokens (128 tokens, 11008 -> 4096, took
+// 24 us with one of 6 stages, 31 us with two of 3). With tokens as M and no split the 37-token
+// call above took 43.6 us.
 //   warp 0    TMA producer            warps 1, 2  MMA issuers, every other block each
 //   warps 3-  promotion: a thread owns one channel and EC tokens. The factors sx*sw (one per token
 //             and block) are put into shared memory for FBLK blocks at a time, which exposes
@@ -104,7 +103,10 @@ struct Cfg {
     static constexpr int FBLK = NT >= 64 ? 16 : 32;              // blocks of factors kept
     static constexpr int RECV = NT * BM * 4;                     // the cluster's sums of this CTA's tokens
     static constexpr int SMEM = 1024 + STAGES * STAGE + RECV + FBLK * NT * 4 + 256;
+    static constexpr int BARRIERS = 2 * STAGES + 2 * ACCS + 3;   // full, empty, acc_full, acc_empty, ...
     static constexpr uint32_t IDESC = umma_idesc_e4m3(BM, NT);
+    static_assert(FBLK * NT == 4 * EPI_THREADS, "four factors per promotion thread");
+    static_assert(BARRIERS <= 32, "a lane sets up each");
     static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024, "CTAs per SM");
     // An issuer waits for its accumulator first: that block it - ACCS has been added tells that the
     // stage's last load (block it - STAGES) landed, so a parity wait on the stage cannot take the
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
     uint64_t* acc_full = empty + C::STAGES;
     uint64_t* acc_empty = acc_full + C::ACCS;
     uint64_t* drained = acc_empty + C::ACCS;
-    uint64_t* recv_full = drained + 2;
+    uint64_t* recv_full = drained + 2;     // the last of BARRIERS in a row
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(recv_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -138,22 +140,6 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
     const int t0 = (tile % p.n_mt) * NT, c0 = (tile / p.n_mt) * f8s::BM;
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.n_kb) * rank / splits);
     const int n_kb = static_cast<int>(static_cast<int64_t>(p.n_kb) * (rank + 1) / splits) - kb0;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < C::ACCS; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], C::EPI_WARPS);
-        }
-        mbar_init(&drained[0], 1);
-        mbar_init(&drained[1], 1);
-        mbar_init(recv_full, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-        mbar_arrive_expect_tx(recv_full, C::RECV);
-    }
     auto load = [&](int it) {      // block it of this CTA into its stage
         const int st = it % C::STAGES;
         uint8_t* sa = smem + st * C::STAGE;
@@ -163,10 +149,38 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
         tma_load_2d(sa + C::A_BYTES, &xmap, &full[st], x, t0);
     };
     const int first = min(C::STAGES, n_kb);
-    if (threadIdx.x == 0) {
-        // the first loads leave while the rest is still being set up
+    // The promotion threads' scales of blocks it0 .. it0 + FBLK - 1, four values each, all asked for at
+    // once (entries past the last block or token repeat the last: they are not used).
+    const int e = static_cast<int>(threadIdx.x) - 96;  // promotion thread
+    float fx[4], fw[4];
+    auto fetch_factors = [&](int it0) {
+        const float* sx = p.sx + static_cast<int64_t>(kb0) * p.n_tok + t0;
+        const float* sw = p.sw + static_cast<int64_t>(c0 / 128) * p.n_kb + kb0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = e + u * C::EPI_THREADS;
+            const int kb = min(it0 + i / NT, n_kb - 1), t = min(i % NT, p.n_tok - 1 - t0);
+            fx[u] = __ldg(sx + static_cast<int64_t>(kb) * p.n_tok + t);
+            fw[u] = __ldg(sw + kb);
+        }
+    };
+    // the first loads leave while the rest is still being set up
+    if (warp == 0) {
+        if (lane < C::BARRIERS) {
+            const int a = lane - 2 * C::STAGES - C::ACCS;            // acc_empty's number, if it is one
+            mbar_init(&full[lane], a >= 0 && a < C::ACCS ? C::EPI_WARPS : 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        if (lane == 0) {
+            *abort_flag = 0;
+            mbar_arrive_expect_tx(recv_full, C::RECV);
+            pdl_wait();
+            for (int it = 0; it < first; ++it) load(it);
+        }
+    } else if (warp >= 3) {
         pdl_wait();
-        for (int it = 0; it < first; ++it) load(it);
+        fetch_factors(0);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -177,7 +191,6 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
     tc_fence_after();
     cluster_arrive();   // this CTA's barriers exist; waited for before anything is sent
     const uint32_t tmem_base = *tmem_slot;
-    pdl_wait();         // nothing the previous kernel may have written was read so far
 
     if (warp == 0) {
         if (lane == 0) {
@@ -232,11 +245,8 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
         __syncwarp();
     } else {
         const int q = warp & 3, g = (warp - 3) >> 2;       // channel quarter, token group
-        const int e = threadIdx.x - 96;                    // promotion thread
         const uint32_t t_addr0 = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                                  static_cast<uint32_t>(g * C::EC);
-        const float* sx = p.sx + static_cast<int64_t>(kb0) * p.n_tok + t0;
-        const float* sw = p.sw + static_cast<int64_t>(c0 / 128) * p.n_kb + kb0;
         float acc[C::EC];
 #pragma unroll
         for (int k = 0; k < C::EC; ++k) acc[k] = 0.0f;
@@ -244,15 +254,12 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
             const int b = it % C::ACCS;
             if (it % C::FBLK == 0) {
                 // the next FBLK blocks' factors, after everybody has used the last ones
-                const int n = min(C::FBLK, n_kb - it) * NT;
-                if (it > 0) asm volatile("bar.sync 1, %0;" ::"n"(C::EPI_THREADS) : "memory");
-#pragma unroll 4
-                for (int i = e; i < n; i += C::EPI_THREADS) {
-                    const int kb = it + i / NT, t = i % NT;
-                    factors[i] = t0 + t < p.n_tok
-                                     ? __ldg(sx + static_cast<int64_t>(kb) * p.n_tok + t) * __ldg(sw + kb)
-                                     : 0.0f;
+                if (it > 0) {
+                    fetch_factors(it);
+                    asm volatile("bar.sync 1, %0;" ::"n"(C::EPI_THREADS) : "memory");
                 }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) factors[e + u * C::EPI_THREADS] = fx[u] * fw[u];
                 asm volatile("bar.sync 1, %0;" ::"n"(C::EPI_THREADS) : "memory");
             }
             // a wait that gave up sets the flag and lets the loop run out: the barriers above
