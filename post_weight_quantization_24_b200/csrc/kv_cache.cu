@@ -72,8 +72,8 @@ __device__ __noinline__ uint2 kv_codes_exact(float4 a, float4 b, float scale, fl
 }
 
 // Eight codes of one chunk. fma(v, inv, magic) holds the integer nearest to v * inv (one rounding).
-// With inv a factor 1 + 2^-22 and 1 - 2^-22 around the correctly rounded 1/scale, v * inv_up and
-// v * inv_dn enclose the exact quotient, so where both round to one integer the quotient does
+// With inv a factor 1 + 2^-22 and 1 - 2^-22 around 1/scale to 2^-23, v * inv_up and v * inv_dn enclose
+// the exact quotient (2^-22 is more than 2^-23 and the two roundings' 2^-24 together), so where both round to one integer the quotient does
 // too; where they differ (one chunk in about 4000 for 4 bits, 300 for 8) the exact decision is
 // made. The lower clamp is implied: rint(lo/s) + rint(-lo/s) = 0.
 template <int BITS>
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
             const float lo = mine.lo(), hi = mine.hi();
             // (a difference with itself is 0 for finite values only)
             const bool finite = (lo - lo) == 0.0f && (hi - hi) == 0.0f;
-            const QParams grid = group_params(finite ? lo : 0.0f, finite ? hi : 0.0f, MAXQ);
+            const QParams grid = group_params_stream(finite ? lo : 0.0f, finite ? hi : 0.0f, MAXQ);
             const bool usable = finite && grid.scale <= 65504.0f;
             const float my_scale = usable ? grid.scale : __uint_as_float(0x7FC00000u);
             const float my_zero = usable ? grid.zero : 0.0f;

@@ -74,6 +74,42 @@ __device__ __forceinline__ QParams group_params(float xmin, float xmax, int maxq
     return p;
 }
 
+// The group scalars of group_params (same values, bit for bit) without branches, for streaming
+// kernels: s = smallest fp16 >= span/maxq (the one fp64 division is the same IEEE
+// operation), z = rint(-lo/s) corrected with the exact residual (ties to even), and an
+// approximate 1/s (relative error <= 2^-23; the codes only use it for a candidate that the
+// caller checks).
+__device__ __forceinline__ QParams group_params_stream(float xmin, float xmax, int maxq) {
+    const double lo = fmin(static_cast<double>(xmin), 0.0);
+    const double hi = fmax(static_cast<double>(xmax), 0.0);
+    const double span = hi - lo;
+    const double q = span / static_cast<double>(maxq);
+    // fp16_ceil(q) for q > 0: spacing 2^(e-10), e = max(floor(log2 q), -14)
+    const long long qb = __double_as_longlong(q);
+    const int e = max(static_cast<int>((qb >> 52) & 0x7FF) - 1023, -14);
+    const double spacing = __longlong_as_double(static_cast<long long>(e - 10 + 1023) << 52);
+    const double inv_spacing = __longlong_as_double(static_cast<long long>(10 - e + 1023) << 52);
+    double sc = ceil(q * inv_spacing) * spacing;
+    sc = (q > 65504.0) ? __longlong_as_double(0x7FF0000000000000LL) : sc;
+    sc = (span == 0.0) ? 1.0 : sc;
+    // z = rint(-lo / sc): candidate, then one exact correction and the tie rule
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(static_cast<float>(sc)));
+    const double nlo = -lo;
+    double k = rint(nlo * static_cast<double>(r));
+    const double e1 = fma(-k, sc, nlo);
+    k += (2.0 * e1 > sc) ? 1.0 : ((2.0 * e1 < -sc) ? -1.0 : 0.0);
+    const double e2 = fma(-k, sc, nlo);
+    const bool tie = (2.0 * e2 == sc || 2.0 * e2 == -sc) && (static_cast<long long>(k) & 1);
+    k += tie ? (e2 > 0.0 ? 1.0 : -1.0) : 0.0;
+    k = isinf(sc) ? 0.0 : k;
+    QParams p;
+    p.scale = static_cast<float>(sc);
+    p.zero = static_cast<float>(k + 0.0);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.inv_scale) : "f"(p.scale));
+    return p;
+}
+
 // The symmetric quantizer (0539edu.com §2.3: zero point fixed at 0, q = round(x/scale)): the
 // range is [-m, m], m = max(|xmin|, |xmax|), split into maxq steps, scale = smallest fp16 >=
 // 2m/maxq (1 for an all-zero group), and the signed zero 0 is stored as the code offset
