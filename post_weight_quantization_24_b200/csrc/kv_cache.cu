@@ -2,17 +2,19 @@
 // (per token and head, groups along head_dim) as they are written into a paged cache, and are
 // read back as scale * (code - zero).
 //
-// Both kernels move each byte once. 16384 tokens x 32 heads x 128, 4 bits, bf16: writing takes 112
-// us (3.1 TB/s; bound by instruction issue, 17 instructions per value, ALU pipe 62 % busy), reading
-// 70 us (4.9 TB/s); 131072 tokens x 8 heads x 128 read in 137 us (5.0 TB/s, five bytes in six of
-// them writes). A decode step's few tokens are bound by launch latency (3 us on the device). A token's heads lie together in the cache, so its
-// n_heads * head_dim elements are one contiguous row in every array. The kernels see plane rows
-// (token 0's keys, token 0's values, token 1's keys, ...) of `wc` chunks of 8 elements; a warp
-// takes 32 consecutive chunks per pass. Where rows are whole multiples of 128 or 64 chunks (1024 or
-// 512 elements), it takes four or two passes of one row at a time (U), which shares a row's
-// addresses among them and the work on the groups' scalars, and keeps 16 U bytes per lane in
-// flight; other widths go pass by pass over row ends (U = 1). A group is 2 to 32 consecutive chunks and never straddles a pass,
-// because it divides both.
+// Both kernels move each byte once. 16384 tokens x 32 heads x 128, 4 bits, bf16: writing takes 100
+// us (3.4 TB/s; bound by instruction issue, 17 instructions per value, ALU pipe 62 % busy), reading
+// 64 us (5.3 TB/s); 131072 tokens x 8 heads x 128 read in @R us (five bytes in six of them
+// writes). A decode step's few tokens are bound by launch latency (3 us on the device).
+//
+// A token's heads lie together in the cache, so its n_heads * head_dim elements are one contiguous
+// row in every array: `wc` chunks of 8 elements, of which a warp takes 32 consecutive ones per
+// pass. Where rows are whole multiples of 128, 64 or 32 chunks (1024, 512 or 256 elements), it
+// takes four, two or one passes of a token's keys and the same of its values at a time (U = 8, 4
+// or 2 passes), which shares the token's addresses among them and the work on the groups' scalars,
+// and keeps 16 U bytes per lane in flight. Other widths go pass by pass over the ends of plane
+// rows (token 0's keys, token 0's values, token 1's keys, ...; U = 1). A group is 2 to 32
+// consecutive chunks and never straddles a pass, because it divides both.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -72,10 +74,11 @@ __device__ __noinline__ uint2 kv_codes_exact(float4 a, float4 b, float scale, fl
 }
 
 // Eight codes of one chunk. fma(v, inv, magic) holds the integer nearest to v * inv (one rounding).
-// With inv a factor 1 + 2^-22 and 1 - 2^-22 around 1/scale to 2^-23, v * inv_up and v * inv_dn enclose
-// the exact quotient (2^-22 is more than 2^-23 and the two roundings' 2^-24 together), so where both round to one integer the quotient does
-// too; where they differ (one chunk in about 4000 for 4 bits, 300 for 8) the exact decision is
-// made. The lower clamp is implied: rint(lo/s) + rint(-lo/s) = 0.
+// inv_up and inv_dn are 1/scale (known to 2^-23) times 1 + 2^-22 and 1 - 2^-22, so v * inv_up and
+// v * inv_dn enclose the exact quotient (2^-22 is more than 2^-23 and the products' roundings of
+// 2^-24 together): where both round to one integer the quotient does too; where they differ (one
+// chunk in about 4000 for 4 bits, 300 for 8) the exact decision is made. The lower clamp is
+// implied: rint(lo/s) + rint(-lo/s) = 0.
 template <int BITS>
 __device__ __forceinline__ uint2 kv_codes(const float* v, const KvGrid& g) {
     constexpr int MAXQ = (1 << BITS) - 1;
@@ -154,10 +157,10 @@ struct KvRange<float> {
 
 // Quantise and write. The ranges of a warp's groups are found with shuffles by the TPG lanes of
 // each, but the groups' scalars (fp64, the dearest part: about 100 instructions) are computed by
-// one lane per group for all four passes at once and handed back with shuffles (the 16384-token
-// call: 174 us with the row's addresses shared by four passes, 129 with the exact decision out of
-// line, 112 with the enclosing roundings; two passes at a time take 144, and loading a unit ahead
-// takes 125, because it costs registers and with them warps).
+// one lane per group for all passes at once and handed back with shuffles. The 16384-token call:
+// 174 us with the addresses shared by four passes, 129 with the exact decision out of line, 111
+// with the enclosing roundings, 109 with branch-free scalars, 100 with eight passes. Tried with four:
+// two 144, loading a unit ahead 125, fewer registers for more warps 120.
 template <typename T, int BITS, int TPG, int U>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restrict__ K,
                                                               const T* __restrict__ V, int64_t n,
@@ -168,12 +171,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
     constexpr int MAXQ = (1 << BITS) - 1, VEC = 8 / Vec<T>::N;
     constexpr int GPP = 32 / TPG;                       // groups of a pass
     constexpr int UR = U * GPP <= 32 ? U : 32 / GPP;    // passes whose groups fit the lanes
+    constexpr int H = U > 1 ? U / 2 : 1;                // passes of the keys, then of the values
     pdl_wait();
     const int lane = lane_id();
     const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x) >> 5;
-    int64_t row = warp0 * (32 * U) / p.wc;              // the warp's plane row and first chunk
-    int wc0 = static_cast<int>(warp0 * (32 * U) - row * p.wc);
-    while (row < 2 * n) {                               // warp-uniform
+    const int64_t n_rows = U > 1 ? n : 2 * n;           // tokens, or plane rows
+    int64_t row = warp0 * (32 * H) / p.wc;              // the warp's row and first chunk
+    int wc0 = static_cast<int>(warp0 * (32 * H) - row * p.wc);
+    while (row < n_rows) {                              // warp-uniform
         int64_t r = row;
         int wc = wc0 + lane;
         if (U == 1) {                                   // a pass may run over row ends
@@ -182,9 +187,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
                 ++r;
             }
         }
-        const int64_t t = r >> 1;
-        const bool is_v = r & 1;
-        int64_t dst = -1;                               // the slot's row in the cache, or -1
+        const int64_t t = U > 1 ? r : r >> 1;
+        int64_t dst = -1;                               // the (first) plane row in the cache, or -1
         uint4 x[U][VEC];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -192,13 +196,15 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
             for (int i = 0; i < VEC; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
         if (U > 1 || t < n) {
             const int64_t slot = __ldg(slots + t);
-            const uint4* src = reinterpret_cast<const uint4*>(
-                (is_v ? V + t * v_stride : K + t * k_stride) + 8 * wc);
+            const uint4* ks = reinterpret_cast<const uint4*>(K + t * k_stride + 8 * wc);
+            const uint4* vs = reinterpret_cast<const uint4*>(V + t * v_stride + 8 * wc);
+            if (U == 1 && (r & 1)) ks = vs;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) x[u][i] = __ldcs(src + u * 32 * VEC + i);
-            if (slot >= 0 && slot < p.n_slots) dst = (is_v ? p.n_slots : 0) + slot;
+                for (int i = 0; i < VEC; ++i)
+                    x[u][i] = __ldcs((u < H ? ks : vs) + (u % H) * 32 * VEC + i);
+            if (slot >= 0 && slot < p.n_slots) dst = (U == 1 && (r & 1) ? p.n_slots : 0) + slot;
             else if (slot >= 0) set_status(p.status, GPTQ_ERR_ARG);
         }
         KvRange<T> range[U];
@@ -239,13 +245,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
                 if constexpr (VEC == 2) Vec<T>::unpack(x[u][1], v + 4);
                 uint2 w = kv_codes<BITS>(v, g);          // (unused where the scale is NaN)
                 if (!good) w = make_uint2(0, 0);
-                const int64_t at = dst * p.wc + wc + 32 * u;
+                const int64_t to = dst + (u < H ? 0 : p.n_slots);
+                const int64_t at = to * p.wc + wc + 32 * (u % H);
                 if (dst >= 0) {
                     if (BITS == 4) reinterpret_cast<uint32_t*>(p.codes)[at] = w.x;
                     else reinterpret_cast<uint2*>(p.codes)[at] = w;
                 }
                 if (lane % TPG == 0 && dst >= 0) {
-                    const int64_t gi = dst * p.ng + (wc + 32 * u) / TPG;
+                    const int64_t gi = to * p.ng + (wc + 32 * (u % H)) / TPG;
                     p.scales[gi] = good ? half_bits(g.scale) : kHalfNan;
                     p.zeros[gi] = half_bits(g.zero);
                 }
@@ -291,7 +298,7 @@ __device__ __forceinline__ void kv_values(uint2 w, float scale, float zero, floa
 }
 
 // Read back. A warp takes `rows` (1 to 32) consecutive tokens: lane i finds token i's sequence,
-// page and slot, and the warp then runs over the tokens' chunks, four passes of loads at a time.
+// page and slot, and the warp then runs over the tokens' chunks, U passes of loads at a time.
 template <typename T, int BITS, int U>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, int page_size,
                                                              int64_t n_pages,
@@ -300,6 +307,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
                                                              const int32_t* __restrict__ cu,
                                                              int64_t total, int rows,
                                                              T* __restrict__ K, T* __restrict__ V) {
+    constexpr int H = U > 1 ? U / 2 : 1;       // passes of the keys, then of the values
     constexpr int64_t kNobody = -2, kMissing = -1;
     pdl_wait();
     const int lane = lane_id();
@@ -323,41 +331,46 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
                 if (mine == kMissing) set_status(p.status, GPTQ_ERR_ARG);
             }
         }
-        const int n_rows = 2 * static_cast<int>(min(static_cast<int64_t>(rows), total - t0));
-        int r = 0, wc = lane;                  // plane row (token, keys or values) and its chunk
-        for (int base = 0; base < n_rows * p.wc; base += 32 * U) {
+        const int n_tok = static_cast<int>(min(static_cast<int64_t>(rows), total - t0));
+        const int n_rows = U > 1 ? n_tok : 2 * n_tok;   // tokens, or plane rows
+        int r = 0, wc = lane;                  // the lane's row and chunk
+        for (int base = 0; base < n_rows * p.wc; base += 32 * H) {
             while (wc >= p.wc) {
                 wc -= p.wc;
                 ++r;
             }
-            const int64_t slot = __shfl_sync(0xffffffffu, mine, (r >> 1) & 31);
+            const int tok = U > 1 ? r : r >> 1;
+            const int64_t slot = __shfl_sync(0xffffffffu, mine, tok & 31);
             if (r < n_rows && slot != kNobody) {
                 uint2 w[U];
                 uint16_t sb[U], zb[U];
-                const int64_t row = ((r & 1) ? p.n_slots : 0) + slot;
+                const int64_t row = (U == 1 && (r & 1) ? p.n_slots : 0) + slot;
                 const int64_t c0 = row * p.wc + wc, g0 = row * p.ng + (wc >> p.tpg_shift);
                 const int g_step = 32 >> p.tpg_shift;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    const int64_t c = c0 + (u < H ? 0 : p.n_slots * p.wc) + 32 * (u % H);
+                    const int64_t g = g0 + (u < H ? 0 : p.n_slots * p.ng) + (u % H) * g_step;
                     w[u] = make_uint2(0, 0);
                     sb[u] = zb[u] = 0;
                     if (slot >= 0) {
-                        if (BITS == 4) w[u].x = __ldg(reinterpret_cast<const uint32_t*>(p.codes) + c0 + 32 * u);
-                        else w[u] = __ldg(reinterpret_cast<const uint2*>(p.codes) + c0 + 32 * u);
-                        sb[u] = __ldg(p.scales + g0 + u * g_step);
-                        zb[u] = __ldg(p.zeros + g0 + u * g_step);
+                        if (BITS == 4) w[u].x = __ldg(reinterpret_cast<const uint32_t*>(p.codes) + c);
+                        else w[u] = __ldg(reinterpret_cast<const uint2*>(p.codes) + c);
+                        sb[u] = __ldg(p.scales + g);
+                        zb[u] = __ldg(p.zeros + g);
                     }
                 }
-                T* out = ((r & 1) ? V : K) + (t0 + (r >> 1)) * p.width + 8 * wc;
+                const int64_t out = (t0 + tok) * p.width + 8 * wc;
+                T* first = (U == 1 && (r & 1) ? V : K) + out;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     float v[8];
                     kv_values<BITS>(w[u], __half2float(__ushort_as_half(sb[u])),
                                     __half2float(__ushort_as_half(zb[u])), v);
-                    kv_store8(out + 256 * u, v);
+                    kv_store8((u < H ? first : V + out) + 256 * (u % H), v);
                 }
             }
-            wc += 32 * U;
+            wc += 32 * H;
         }
         __syncwarp();
     }
@@ -366,8 +379,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
 template <typename T, int BITS, int TPG, int U>
 static gptq_status kv_write_go(const T* K, const T* V, int64_t n, int64_t ks, int64_t vs,
                                const int64_t* slots, const KvParams& p, cudaStream_t s) {
-    constexpr int64_t kChunks = 32 * U * (kKvThreads / 32);       // of a CTA
-    const int64_t want = (2 * n * p.wc + kChunks - 1) / kChunks;
+    constexpr int64_t kChunks = 32 * (U > 1 ? U / 2 : 1) * (kKvThreads / 32);   // of a CTA's rows
+    const int64_t want = ((U > 1 ? n : 2 * n) * p.wc + kChunks - 1) / kChunks;
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 16));
     const int64_t stride = grid * kChunks;
     GPTQ_CUDA_TRY(launch_pdl(kv_write_kernel<T, BITS, TPG, U>, dim3(grid), dim3(kKvThreads), 0, s, K, V,
@@ -394,14 +407,19 @@ static gptq_status kv_write_launch(const void* K, const void* V, int64_t n, int6
                                    cudaStream_t s) {
     const T* k = static_cast<const T*>(K);
     const T* v = static_cast<const T*>(V);
-    if (p.wc % 128 == 0)
-        return bits == 4 ? kv_write_group<T, 4, 4>(k, v, n, ks, vs, slots, p, s)
-                         : kv_write_group<T, 8, 4>(k, v, n, ks, vs, slots, p, s);
-    if (p.wc % 64 == 0)
-        return bits == 4 ? kv_write_group<T, 4, 2>(k, v, n, ks, vs, slots, p, s)
-                         : kv_write_group<T, 8, 2>(k, v, n, ks, vs, slots, p, s);
-    return bits == 4 ? kv_write_group<T, 4, 1>(k, v, n, ks, vs, slots, p, s)
-                     : kv_write_group<T, 8, 1>(k, v, n, ks, vs, slots, p, s);
+#define KV_WRITE(U)                                                             \
+    (bits == 4 ? kv_write_group<T, 4, U>(k, v, n, ks, vs, slots, p, s) \
+               : kv_write_group<T, 8, U>(k, v, n, ks, vs, slots, p, s))
+    // Eight passes where their groups fit the warp's lanes (from 64 elements; groups of 32 take 62
+    // us with eight and 57 with four at 16384 x 16 x 128), and only as many as leave 16 units for
+    // every SM: 64 tokens x 32 x 128 take 6.1 us with eight passes and 4.2 with two, 256 tokens
+    // x 32 x 128 6.2 with four and 5.2 with two, 16384 x 32 x 128 100 us with eight, 109 with four.
+    const int64_t units2 = n * p.wc / 32, enough = static_cast<int64_t>(num_sms()) * 16;
+    if (p.wc % 128 == 0 && p.tpg_shift >= 3 && units2 >= 4 * enough) return KV_WRITE(8);
+    if (p.wc % 64 == 0 && units2 >= 2 * enough) return KV_WRITE(4);
+    if (p.wc % 32 == 0) return KV_WRITE(2);
+    return KV_WRITE(1);
+#undef KV_WRITE
 }
 
 template <typename T>
@@ -418,9 +436,16 @@ static gptq_status kv_read_launch(const KvParams& p, int page_size, int64_t n_pa
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 64));
     T* k = static_cast<T*>(K);
     T* v = static_cast<T*>(V);
-    auto* kernel = p.wc % 128 == 0  ? (bits == 4 ? kv_read_kernel<T, 4, 4> : kv_read_kernel<T, 8, 4>)
-                   : p.wc % 64 == 0 ? (bits == 4 ? kv_read_kernel<T, 4, 2> : kv_read_kernel<T, 8, 2>)
-                                    : (bits == 4 ? kv_read_kernel<T, 4, 1> : kv_read_kernel<T, 8, 1>);
+#define KV_READ(U) (bits == 4 ? kv_read_kernel<T, 4, U> : kv_read_kernel<T, 8, U>)
+    // As many bytes in flight as pay: 16384 x 32 x 128 in bf16 takes 64 us with eight passes and 70
+    // with four at 4 bits, 80 and 74 at 8; 16384 x 8 x 128 in fp32 (which writes twice as much per
+    // chunk) 40 us with eight or four and 36 with two.
+    const bool half = sizeof(T) == 2;
+    auto* kernel = p.wc % 128 == 0 && bits == 4 && half ? KV_READ(8)
+                   : p.wc % 64 == 0 && half             ? KV_READ(4)
+                   : p.wc % 32 == 0                     ? KV_READ(2)
+                                                        : KV_READ(1);
+#undef KV_READ
     GPTQ_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kKvThreads), 0, s, p, page_size, n_pages, table,
                              n_seqs, max_pages, cu, total, rows, k, v));
     GPTQ_LAUNCHED();

@@ -71,6 +71,34 @@ def test_write_matches_the_oracle(cuda_lib, n, H, D, bits, g, page, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("H,D,bits,g", [
+    (8, 128, 4, 64), (8, 128, 8, 128), (4, 256, 8, 256), (8, 128, 4, 32), (8, 128, 8, 16),
+    (4, 128, 4, 128), (4, 128, 8, 32), (4, 128, 4, 16), (2, 128, 4, 64), (3, 80, 8, 16)])
+def test_a_long_write_is_many_short_ones(cuda_lib, H, D, bits, g, dtype):
+    """Thousands of tokens in one call leave the cache bit for bit as calls of 100 tokens do, and
+    those are checked against the oracle above; the last tokens against the oracle here too."""
+    page, n = 64, 5003
+    n_pages = n // page + 3
+    one, host = _filled(cuda_lib, n_pages, page, H, D, bits, g, seed=5)
+    many = [t.clone() for t in one]
+    K, V = _kv(n, H, D, dtype, seed=D + H)
+    K[7, 0, 3], V[n - 2, H - 1, D - 1] = float("nan"), float("inf")
+    perm = torch.randperm(n_pages * page, generator=torch.Generator().manual_seed(H))[:n]
+    perm[5::50] = -1
+    kd, vd, pd = K.cuda(), V.cuda(), perm.cuda()
+    cuda_lib.kv_cache_write(kd, vd, pd, *one, bits=bits)
+    for i in range(0, n, 100):
+        cuda_lib.kv_cache_write(kd[i:i + 100], vd[i:i + 100], pd[i:i + 100], *many, bits=bits)
+    for a, b in zip(one, many):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    okv.write(*host, _np(K[-40:]), _np(V[-40:]), perm[-40:].tolist(), bits)
+    slots = perm[-40:][perm[-40:] >= 0].numpy()
+    for d, h in zip(one, host):
+        _same(d.cpu().numpy().reshape(2, n_pages * page, -1)[:, slots],
+              h.reshape(2, n_pages * page, -1)[:, slots])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("H,D,bits,g,page", SHAPES)
 def test_read_matches_the_oracle(cuda_lib, H, D, bits, g, page, dtype):
     """Ragged lengths with empty sequences at the start, inside and at the end; pages that end
