@@ -298,22 +298,25 @@ __device__ __forceinline__ void kv_values(uint2 w, float scale, float zero, floa
 }
 
 // Read back. A warp takes `rows` (1 to 32) consecutive tokens: lane i finds token i's sequence,
-// page and slot, and the warp then runs over the tokens' chunks, U passes of loads at a time.
+// page and slot, and the warp then runs over the tokens' chunks, U passes of loads at a time. Of few and wide
+// tokens the warps of a CTA share each (1 << log_parts of them).
 template <typename T, int BITS, int U>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, int page_size,
                                                              int64_t n_pages,
                                                              const int32_t* __restrict__ table,
                                                              int n_seqs, int max_pages,
                                                              const int32_t* __restrict__ cu,
-                                                             int64_t total, int rows,
+                                                             int64_t total, int rows, int log_parts,
                                                              T* __restrict__ K, T* __restrict__ V) {
     constexpr int H = U > 1 ? U / 2 : 1;       // passes of the keys, then of the values
     constexpr int64_t kNobody = -2, kMissing = -1;
     pdl_wait();
     const int lane = lane_id();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kKvThreads / 32) * rows;
-    for (int64_t t0 = ((static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x) >> 5) * rows;
-         t0 < total; t0 += step) {
+    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x) >> 5;
+    const int parts = 1 << log_parts;          // warps of a token, all of one CTA
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ((kKvThreads / 32) >> log_parts) * rows;
+    const int first_chunk = static_cast<int>(warp & (parts - 1)) * 32 * H;
+    for (int64_t t0 = (warp >> log_parts) * rows; t0 < total; t0 += step) {
         int64_t mine = kNobody;
         if (lane < rows && t0 + lane < total) {
             const int b = kv_find_seq(cu, n_seqs, t0 + lane);
@@ -333,8 +336,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
         }
         const int n_tok = static_cast<int>(min(static_cast<int64_t>(rows), total - t0));
         const int n_rows = U > 1 ? n_tok : 2 * n_tok;   // tokens, or plane rows
-        int r = 0, wc = lane;                  // the lane's row and chunk
-        for (int base = 0; base < n_rows * p.wc; base += 32 * H) {
+        int r = 0, wc = first_chunk + lane;    // the lane's row and chunk
+        for (int base = first_chunk; base < n_rows * p.wc; base += parts * 32 * H) {
             while (wc >= p.wc) {
                 wc -= p.wc;
                 ++r;
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
                     kv_store8((u < H ? first : V + out) + 256 * (u % H), v);
                 }
             }
-            wc += 32 * H;
+            wc += parts * 32 * H;
         }
         __syncwarp();
     }
@@ -431,7 +434,12 @@ static gptq_status kv_read_launch(const KvParams& p, int page_size, int64_t n_pa
     const int64_t warps = static_cast<int64_t>(num_sms()) * 32;
     int rows = 1;
     while (rows < 32 && 2 * rows * warps <= total) rows *= 2;
-    const int64_t per_cta = rows * (kKvThreads / 32);
+    // where tokens are scarcer still, two or four warps take a wide token's passes in turn (101
+    // tokens x 32 x 128 take 3.2 us so, 4.2 with two warps and 5.2 with one)
+    int log_parts = 0;
+    while (log_parts < 2 && (2 * total << log_parts) <= warps && (128 << log_parts) < p.wc)
+        ++log_parts;
+    const int64_t per_cta = rows * ((kKvThreads / 32) >> log_parts);
     const int64_t want = (total + per_cta - 1) / per_cta;
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 64));
     T* k = static_cast<T*>(K);
@@ -447,7 +455,7 @@ static gptq_status kv_read_launch(const KvParams& p, int page_size, int64_t n_pa
                                                         : KV_READ(1);
 #undef KV_READ
     GPTQ_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kKvThreads), 0, s, p, page_size, n_pages, table,
-                             n_seqs, max_pages, cu, total, rows, k, v));
+                             n_seqs, max_pages, cu, total, rows, log_parts, k, v));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }
