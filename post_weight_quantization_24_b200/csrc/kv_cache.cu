@@ -2,10 +2,10 @@
 // (per token and head, groups along head_dim) as they are written into a paged cache, and are
 // read back as scale * (code - zero).
 //
-// Both kernels move each byte once. 16384 tokens x 32 heads x 128, 4 bits, bf16: writing takes 100
-// us (3.4 TB/s; bound by instruction issue, 17 instructions per value, ALU pipe 62 % busy), reading
-// 64 us (5.3 TB/s); 131072 tokens x 8 heads x 128 read in @R us (five bytes in six of them
-// writes). A decode step's few tokens are bound by launch latency (3 us on the device).
+// Both kernels move each byte once. 16384 tokens x 32 heads x 128, 4 bits, bf16: writing takes 64 us
+// (5.3 TB/s, 0.81 of the copy rate), reading 64 us (5.3 TB/s); 131072 tokens x 8 heads x 128 read in
+// 126 us (5.5 TB/s, five bytes in six of them writes). A decode step's few tokens are bound by
+// launch latency (3 us on the device).
 //
 // A token's heads lie together in the cache, so its n_heads * head_dim elements are one contiguous
 // row in every array: `wc` chunks of 8 elements, of which a warp takes 32 consecutive ones per
@@ -45,10 +45,12 @@ __device__ __forceinline__ void kv_store8(T* p, const float* v) {
 constexpr uint16_t kHalfNan = 0x7E00;
 constexpr float kMagicInt = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, half to even
 
-// A group's grid as the code loop uses it: 1/scale a little up and down, and what turns the bits of
-// kMagicInt + k into the code k + zero.
+// A group's grid as the code loop uses it: 1/scale, and what turns the bits of a rounded quotient
+// into its code (scale and zero for the exact decision only).
 struct KvGrid {
-    float scale, zero, inv_up, inv_dn;
+    float inv;
+    int to_code;
+    float scale, zero;
 };
 
 // Eight codes (0 .. MAXQ) packed. BITS == 4: one word; 8: two.
@@ -74,24 +76,37 @@ __device__ __noinline__ uint2 kv_codes_exact(float4 a, float4 b, float scale, fl
 }
 
 // Eight codes of one chunk. fma(v, inv, magic) holds the integer nearest to v * inv (one rounding).
-// inv_up and inv_dn are 1/scale (known to 2^-23) times 1 + 2^-22 and 1 - 2^-22, so v * inv_up and
-// v * inv_dn enclose the exact quotient (2^-22 is more than 2^-23 and the products' roundings of
-// 2^-24 together): where both round to one integer the quotient does too; where they differ (one
-// chunk in about 4000 for 4 bits, 300 for 8) the exact decision is made. The lower clamp is
-// implied: rint(lo/s) + rint(-lo/s) = 0.
-template <int BITS>
+// up and dn are 1/scale (known to 2^-23) times 1 + 2^-22 and 1 - 2^-22, so v * up and v * dn enclose
+// the exact quotient, each within 2^-21 of it (2^-22, 2^-23 and the products' roundings of
+// 2^-24): where both round to one integer the quotient does too.
+//   16-bit types: where they differ the quotient is a tie, and the even one of the two is taken:
+//   the sum of the two rounded values, (2 magic + k + k') of spacing 2, rounds to it by itself.
+//   For with v = m 2^a and scale = M 2^b (M < 2^11), a quotient other than k + 1/2 is off it by
+//   |2v - (2k+1) scale| / (2v) of itself, which is at least 2^min(a+1,b) / (2v): 2^-11 where a + 1
+//   < b, else 1 / (2 (k+1/2) M) > 2^-20 for k up to 255.
+//   fp32: the exact decision is made (one chunk in about 4000 for 4 bits, 300 for 8).
+// Ties are not rare: one warp's pass in seven has one in bf16, where the scales often end in
+// zeros (deciding them out of line took 4 % more).
+// The lower clamp is implied: rint(lo/s) + rint(-lo/s) = 0.
+template <typename T, int BITS>
 __device__ __forceinline__ uint2 kv_codes(const float* v, const KvGrid& g) {
     constexpr int MAXQ = (1 << BITS) - 1;
-    // bits(magic) = 0x4B400000; bits(magic + zero) less twice that, added to bits(magic + k), is k + zero
-    const int to_code = static_cast<int>(__float_as_uint(kMagicInt + g.zero) - 0x96800000u);
+    auto twice = [](float x) { return f32x2(__float_as_uint(x), __float_as_uint(x)); };
+    const uint64_t up2 = twice(g.inv * (1.0f + 0x1p-22f)), dn2 = twice(g.inv * (1.0f - 0x1p-22f));
     int q[8];
     uint32_t differ = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int up = __float_as_int(fmaf(v[i], g.inv_up, kMagicInt));
-        const int dn = __float_as_int(fmaf(v[i], g.inv_dn, kMagicInt));
-        differ |= static_cast<uint32_t>(up ^ dn);
-        q[i] = __viaddmin_s32(up, to_code, MAXQ);
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t v2 = f32x2(__float_as_uint(v[i]), __float_as_uint(v[i + 1]));
+        uint64_t a = twice(kMagicInt), b = twice(kMagicInt);
+        fma_f32x2(a, v2, up2);
+        fma_f32x2(b, v2, dn2);
+        if (sizeof(T) == 4)
+            differ |= static_cast<uint32_t>(a ^ b) | static_cast<uint32_t>((a ^ b) >> 32);
+        fma_f32x2(b, a, twice(1.0f));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            q[i + j] = __viaddmin_s32(__float_as_int(f32x2_get(b, j)), g.to_code, MAXQ);
     }
     if (differ)
         return kv_codes_exact<BITS>(make_float4(v[0], v[1], v[2], v[3]),
@@ -99,37 +114,52 @@ __device__ __forceinline__ uint2 kv_codes(const float* v, const KvGrid& g) {
     return pack_codes<BITS>(q);
 }
 
+// to_code of a zero: 2 magic + 2 k has the bits 0x4BC00000 + k, magic + zero 0x4B400000 + zero.
+__device__ __forceinline__ int kv_to_code(float zero) {
+    return static_cast<int>(__float_as_uint(kMagicInt + zero) - 0x97000000u);
+}
+
 // A range {minimum, -maximum} of a chunk or group, so that one minimum joins both ends; NaN if any
-// value is. In the 16-bit types it is one packed register.
+// value is. In the 16-bit types it is one packed register. or_if(c, o) is o where c holds.
 template <typename T>
 struct KvRange;
 template <>
 struct KvRange<__half> {
-    __half2 r;
+    uint32_t r;
+    __device__ __forceinline__ __half2 pair() const { return *reinterpret_cast<const __half2*>(&r); }
+    __device__ __forceinline__ void set(__half2 x) { r = *reinterpret_cast<const uint32_t*>(&x); }
     __device__ __forceinline__ void of(const uint4* x) {
         __half2 a, b;
         minmax_packed(x[0], a, b);
-        r = __halves2half2(__hmin_nan(__low2half(a), __high2half(a)),
-                           __hneg(__hmax_nan(__low2half(b), __high2half(b))));
+        set(__halves2half2(__hmin_nan(__low2half(a), __high2half(a)),
+                          __hneg(__hmax_nan(__low2half(b), __high2half(b)))));
     }
-    __device__ __forceinline__ void join(int o) { r = __hmin2_nan(r, __shfl_xor_sync(0xffffffffu, r, o)); }
-    __device__ __forceinline__ KvRange from(int lane) const { return {__shfl_sync(0xffffffffu, r, lane)}; }
-    __device__ __forceinline__ float lo() const { return __low2float(r); }
-    __device__ __forceinline__ float hi() const { return -__high2float(r); }
+    __device__ __forceinline__ void join(const KvRange& o) { set(__hmin2_nan(pair(), o.pair())); }
+    __device__ __forceinline__ KvRange other(int mask) const {
+        return {__shfl_xor_sync(0xffffffffu, r, mask)};
+    }
+    __device__ __forceinline__ KvRange or_if(bool c, const KvRange& o) const { return {c ? o.r : r}; }
+    __device__ __forceinline__ float lo() const { return __low2float(pair()); }
+    __device__ __forceinline__ float hi() const { return -__high2float(pair()); }
 };
 template <>
 struct KvRange<__nv_bfloat16> {
-    __nv_bfloat162 r;
+    uint32_t r;
+    __device__ __forceinline__ __nv_bfloat162 pair() const { return *reinterpret_cast<const __nv_bfloat162*>(&r); }
+    __device__ __forceinline__ void set(__nv_bfloat162 x) { r = *reinterpret_cast<const uint32_t*>(&x); }
     __device__ __forceinline__ void of(const uint4* x) {
         __nv_bfloat162 a, b;
         minmax_packed(x[0], a, b);
-        r = __halves2bfloat162(__hmin_nan(__low2bfloat16(a), __high2bfloat16(a)),
-                               __hneg(__hmax_nan(__low2bfloat16(b), __high2bfloat16(b))));
+        set(__halves2bfloat162(__hmin_nan(__low2bfloat16(a), __high2bfloat16(a)),
+                              __hneg(__hmax_nan(__low2bfloat16(b), __high2bfloat16(b)))));
     }
-    __device__ __forceinline__ void join(int o) { r = __hmin2_nan(r, __shfl_xor_sync(0xffffffffu, r, o)); }
-    __device__ __forceinline__ KvRange from(int lane) const { return {__shfl_sync(0xffffffffu, r, lane)}; }
-    __device__ __forceinline__ float lo() const { return __low2float(r); }
-    __device__ __forceinline__ float hi() const { return -__high2float(r); }
+    __device__ __forceinline__ void join(const KvRange& o) { set(__hmin2_nan(pair(), o.pair())); }
+    __device__ __forceinline__ KvRange other(int mask) const {
+        return {__shfl_xor_sync(0xffffffffu, r, mask)};
+    }
+    __device__ __forceinline__ KvRange or_if(bool c, const KvRange& o) const { return {c ? o.r : r}; }
+    __device__ __forceinline__ float lo() const { return __low2float(pair()); }
+    __device__ __forceinline__ float hi() const { return -__high2float(pair()); }
 };
 template <>
 struct KvRange<float> {
@@ -144,22 +174,29 @@ struct KvRange<float> {
             nmx = min_nan(nmx, -__uint_as_float(w[i]));
         }
     }
-    __device__ __forceinline__ void join(int o) {
-        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        nmx = min_nan(nmx, __shfl_xor_sync(0xffffffffu, nmx, o));
+    __device__ __forceinline__ void join(const KvRange& o) {
+        mn = min_nan(mn, o.mn);
+        nmx = min_nan(nmx, o.nmx);
     }
-    __device__ __forceinline__ KvRange from(int lane) const {
-        return {__shfl_sync(0xffffffffu, mn, lane), __shfl_sync(0xffffffffu, nmx, lane)};
+    __device__ __forceinline__ KvRange other(int mask) const {
+        return {__shfl_xor_sync(0xffffffffu, mn, mask), __shfl_xor_sync(0xffffffffu, nmx, mask)};
+    }
+    __device__ __forceinline__ KvRange or_if(bool c, const KvRange& o) const {
+        return {c ? o.mn : mn, c ? o.nmx : nmx};
     }
     __device__ __forceinline__ float lo() const { return mn; }
     __device__ __forceinline__ float hi() const { return -nmx; }
 };
 
-// Quantise and write. The ranges of a warp's groups are found with shuffles by the TPG lanes of
-// each, but the groups' scalars (fp64, the dearest part: about 100 instructions) are computed by
-// one lane per group for all passes at once and handed back with shuffles. The 16384-token call:
-// 174 us with the addresses shared by four passes, 129 with the exact decision out of line, 111
-// with the enclosing roundings, 109 with branch-free scalars, 100 with eight passes. Tried with four:
+// Quantise and write. The TPG lanes of a group join their U passes' ranges in halves: at each step a
+// lane keeps one half of the passes that it still holds and hands the other half to its partner,
+// so that it ends with whole ranges of ROUNDS passes, no two lanes with the same while U >= TPG,
+// for U - 1 shuffles instead of U log2(TPG). Each lane computes the scalars of its own (fp64, the
+// dearest part: about 100 instructions) and writes scale and zero; the lanes of a group fetch what
+// they need for their codes with two shuffles per pass.
+// 16384 tokens x 32 x 128, 4 bits, bf16: 64 us. On the way there: 174 us with the addresses shared
+// by four passes, 129 with the exact decision out of line, 111 with the enclosing roundings, 109
+// with branch-free scalars, 100 with eight passes, 96 with ties in line. Tried with four passes:
 // two 144, loading a unit ahead 125, fewer registers for more warps 120.
 template <typename T, int BITS, int TPG, int U>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restrict__ K,
@@ -169,8 +206,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
                                                               const KvParams p, int64_t row_step,
                                                               int wc_step) {
     constexpr int MAXQ = (1 << BITS) - 1, VEC = 8 / Vec<T>::N;
-    constexpr int GPP = 32 / TPG;                       // groups of a pass
-    constexpr int UR = U * GPP <= 32 ? U : 32 / GPP;    // passes whose groups fit the lanes
+    constexpr int ROUNDS = U > TPG ? U / TPG : 1;       // passes whose scalars a lane computes
     constexpr int H = U > 1 ? U / 2 : 1;                // passes of the keys, then of the values
     pdl_wait();
     const int lane = lane_id();
@@ -209,52 +245,60 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const T* __restric
         }
         KvRange<T> range[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            range[u].of(x[u]);
+        for (int u = 0; u < U; ++u) range[u].of(x[u]);
+        int mine = 0;                                   // the lane's (first) pass
 #pragma unroll
-            for (int o = TPG / 2; o > 0; o >>= 1) range[u].join(o);
+        for (int o = 1; o < TPG; o *= 2) {
+            const int half = U / (2 * o);               // 0: one pass left, joined by all lanes
+            const bool upper = half > 0 && (lane & o);
+            if (upper) mine += half;
+#pragma unroll
+            for (int u = 0; u < (half > 0 ? half : 1); ++u) {
+                const KvRange<T> give = range[u + half].or_if(upper, range[u]);
+                range[u] = range[u].or_if(upper, range[u + half]);
+                range[u].join(give.other(o));
+            }
         }
 #pragma unroll
-        for (int u0 = 0; u0 < U; u0 += UR) {
-            // lane l computes the grid of pass u0 + l / GPP, group l % GPP
-            KvRange<T> mine = range[u0].from((lane % GPP) * TPG);
-#pragma unroll
-            for (int u = 1; u < UR; ++u) {
-                const KvRange<T> other = range[u0 + u].from((lane % GPP) * TPG);
-                if (lane / GPP == u) mine = other;
-            }
-            const float lo = mine.lo(), hi = mine.hi();
+        for (int j = 0; j < ROUNDS; ++j) {
+            const float lo = range[j].lo(), hi = range[j].hi();
             // (a difference with itself is 0 for finite values only)
             const bool finite = (lo - lo) == 0.0f && (hi - hi) == 0.0f;
             const QParams grid = group_params_stream(finite ? lo : 0.0f, finite ? hi : 0.0f, MAXQ);
             const bool usable = finite && grid.scale <= 65504.0f;
-            const float my_scale = usable ? grid.scale : __uint_as_float(0x7FC00000u);
-            const float my_zero = usable ? grid.zero : 0.0f;
+            const float zero = usable ? grid.zero : 0.0f;
+            const float inv = usable ? grid.inv_scale : __uint_as_float(0x7FC00000u);
+            const int to_code = kv_to_code(zero);
+            if (dst >= 0 && lane % TPG < U) {
+                const int u = mine + j;
+                const int64_t to = dst + (u < H ? 0 : p.n_slots);
+                const int64_t gi = to * p.ng + (wc + 32 * (u % H)) / TPG;
+                p.scales[gi] = usable ? half_bits(grid.scale) : kHalfNan;
+                p.zeros[gi] = half_bits(zero);
+            }
 #pragma unroll
-            for (int u = u0; u < u0 + UR; ++u) {
-                const int src = (u - u0) * GPP + lane / TPG;
-                const float inv = __shfl_sync(0xffffffffu, grid.inv_scale, src);
+            for (int u = j; u < U; u += ROUNDS) {
+                int src = 0;                            // the group's lane that has pass u
+#pragma unroll
+                for (int o = 1; o < TPG && U / (2 * o) > 0; o *= 2)
+                    if (u & (U / (2 * o))) src += o;
                 KvGrid g;
-                g.scale = __shfl_sync(0xffffffffu, my_scale, src);
-                g.zero = __shfl_sync(0xffffffffu, my_zero, src);
-                g.inv_up = inv * (1.0f + 0x1p-22f);
-                g.inv_dn = inv * (1.0f - 0x1p-22f);
-                const bool good = g.scale == g.scale;
+                g.inv = __shfl_sync(0xffffffffu, inv, src, TPG);
+                g.to_code = __shfl_sync(0xffffffffu, to_code, src, TPG);
+                if (sizeof(T) == 4) {
+                    g.scale = __shfl_sync(0xffffffffu, grid.scale, src, TPG);
+                    g.zero = __shfl_sync(0xffffffffu, zero, src, TPG);
+                }
                 float v[8];
                 Vec<T>::unpack(x[u][0], v);
                 if constexpr (VEC == 2) Vec<T>::unpack(x[u][1], v + 4);
-                uint2 w = kv_codes<BITS>(v, g);          // (unused where the scale is NaN)
-                if (!good) w = make_uint2(0, 0);
-                const int64_t to = dst + (u < H ? 0 : p.n_slots);
-                const int64_t at = to * p.wc + wc + 32 * (u % H);
+                uint2 w = kv_codes<T, BITS>(v, g);
+                if (!(g.inv == g.inv)) w = make_uint2(0, 0);    // no finite grid: codes 0
                 if (dst >= 0) {
+                    const int64_t to = dst + (u < H ? 0 : p.n_slots);
+                    const int64_t at = to * p.wc + wc + 32 * (u % H);
                     if (BITS == 4) reinterpret_cast<uint32_t*>(p.codes)[at] = w.x;
                     else reinterpret_cast<uint2*>(p.codes)[at] = w;
-                }
-                if (lane % TPG == 0 && dst >= 0) {
-                    const int64_t gi = to * p.ng + (wc + 32 * (u % H)) / TPG;
-                    p.scales[gi] = good ? half_bits(g.scale) : kHalfNan;
-                    p.zeros[gi] = half_bits(g.zero);
                 }
             }
         }
@@ -413,10 +457,9 @@ static gptq_status kv_write_launch(const void* K, const void* V, int64_t n, int6
 #define KV_WRITE(U)                                                             \
     (bits == 4 ? kv_write_group<T, 4, U>(k, v, n, ks, vs, slots, p, s) \
                : kv_write_group<T, 8, U>(k, v, n, ks, vs, slots, p, s))
-    // Eight passes where their groups fit the warp's lanes (from 64 elements; groups of 32 take 62
-    // us with eight and 57 with four at 16384 x 16 x 128), and only as many as leave 16 units for
-    // every SM: 64 tokens x 32 x 128 take 6.1 us with eight passes and 4.2 with two, 256 tokens
-    // x 32 x 128 6.2 with four and 5.2 with two, 16384 x 32 x 128 100 us with eight, 109 with four.
+    // Eight passes where a group's lanes are as many (64 elements), and only as many as leave 16
+    // units for every SM: 64 tokens x 32 x 128 take 6.1 us with eight passes and 4.2 with two, 256
+    // tokens 6.2 with four and 5.2 with two, 16384 tokens 64 with eight, 7@ with four.
     const int64_t units2 = n * p.wc / 32, enough = static_cast<int64_t>(num_sms()) * 16;
     if (p.wc % 128 == 0 && p.tpg_shift >= 3 && units2 >= 4 * enough) return KV_WRITE(8);
     if (p.wc % 64 == 0 && units2 >= 2 * enough) return KV_WRITE(4);
