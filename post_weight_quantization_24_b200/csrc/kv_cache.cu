@@ -2,9 +2,9 @@
 // (per token and head, groups along head_dim) as they are written into a paged cache, and are
 // read back as scale * (code - zero).
 //
-// Both kernels move each byte once. 16384 tokens x 32 heads x 128, 4 bits, bf16: writing takes 64 us
-// (5.3 TB/s, 0.81 of the copy rate), reading 64 us (5.3 TB/s); 131072 tokens x 8 heads x 128 read in
-// 126 us (5.5 TB/s, five bytes in six of them writes). A decode step's few tokens are bound by
+// Both kernels move each byte once. 16384 tokens x 32 heads x 128, 4 bits, bf16: writing takes 60 us
+// (5.7 TB/s, 0.87 of the copy rate), reading 60 us (5.8 TB/s); 131072 tokens x 8 heads x 128 read in
+// 114 us (6.0 TB/s, five bytes in six of them writes). A decode step's few tokens are bound by
 // launch latency (3 us on the device).
 //
 // A token's heads lie together in the cache, so its n_heads * head_dim elements are one contiguous
@@ -16,6 +16,7 @@
 // rows (token 0's keys, token 0's values, token 1's keys, ...; U = 1). A group is 2 to 32
 // consecutive chunks and never straddles a pass, because it divides both.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.cuh"
 #include "quant.cuh"
@@ -36,10 +37,21 @@ struct KvParams {
 
 constexpr int kKvThreads = 128;
 
+// fp32 goes out as one store of 32 bytes per lane where rows start on such boundaries: two of 16,
+// each touching half of every 32-byte sector, took 15 % more.
+__device__ __forceinline__ void kv_store8(float* p, const float* v, int wide) {
+    if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+                     "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4*>(p) = Vec<float>::pack(v);
+        *(reinterpret_cast<uint4*>(p) + 1) = Vec<float>::pack(v + 4);
+    }
+}
 template <typename T>
-__device__ __forceinline__ void kv_store8(T* p, const float* v) {
+__device__ __forceinline__ void kv_store8(T* p, const float* v, int) {
     *reinterpret_cast<uint4*>(p) = Vec<T>::pack(v);
-    if constexpr (Vec<T>::N == 4) *(reinterpret_cast<uint4*>(p) + 1) = Vec<T>::pack(v + 4);
 }
 
 constexpr uint16_t kHalfNan = 0x7E00;
@@ -194,7 +206,7 @@ struct KvRange<float> {
 // for U - 1 shuffles instead of U log2(TPG). Each lane computes the scalars of its own (fp64, the
 // dearest part: about 100 instructions) and writes scale and zero; the lanes of a group fetch what
 // they need for their codes with two shuffles per pass.
-// 16384 tokens x 32 x 128, 4 bits, bf16: 64 us. On the way there: 174 us with the addresses shared
+// 16384 tokens x 32 x 128, 4 bits, bf16: 60 us. On the way there: 174 us with the addresses shared
 // by four passes, 129 with the exact decision out of line, 111 with the enclosing roundings, 109
 // with branch-free scalars, 100 with eight passes, 96 with ties in line. Tried with four passes:
 // two 144, loading a unit ahead 125, fewer registers for more warps 120.
@@ -322,28 +334,65 @@ __device__ __forceinline__ int kv_find_seq(const int32_t* __restrict__ cu, int n
     return lo;
 }
 
-// Eight values of one chunk. A code becomes the fp32 2^23 + code by placing its byte into a
-// constant; the difference to 2^23 + zero is exact, and so is the product with the fp16 scale.
-template <int BITS>
-__device__ __forceinline__ void kv_values(uint2 w, float scale, float zero, float* v) {
-    const float z = 8388608.0f + zero;
-    uint32_t a = w.x, b = w.y;
-    if (BITS == 4) {
-        b = (w.x >> 4) & 0x0F0F0F0Fu;          // odd elements
-        a = w.x & 0x0F0F0F0Fu;                 // even elements
-    }
+// Eight values of one chunk, scale * (code - zero) rounded once to T. A code's byte is placed into
+// the mantissa of a constant, and two values go through one instruction:
+//   fp16          1024 + code, less 1024 + zero (exact), times scale
+//   else, 4 bits  fma(128 + code, scale, -scale (128 + zero)): 8 and 11 bits, so the products and
+//                 their difference are exact in fp32
+//   else, 8 bits  2^23 + code, less 2^23 + zero (exact), times scale (exact: 9 and 11 bits)
+template <typename T, int BITS>
+__device__ __forceinline__ void kv_values(uint2 w, uint16_t scale_bits, uint16_t zero_bits, T* at,
+                                          int wide) {
+    const uint32_t even = w.x & 0x0F0F0F0Fu, odd = (w.x >> 4) & 0x0F0F0F0Fu;     // for 4 bits
+    const __half hs = __ushort_as_half(scale_bits), hz = __ushort_as_half(zero_bits);
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 s2 = __half2half2(hs);
+        const __half2 z2 = __half2half2(__hadd(hz, __ushort_as_half(0x6400)));
+        const uint32_t lo = BITS == 4 ? __byte_perm(even, odd, 0x5140) : w.x;
+        const uint32_t hi = BITS == 4 ? __byte_perm(even, odd, 0x7362) : w.y;
+        uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x = __uint_as_float(__byte_perm(a, 0x4B000000u, 0x7540 + i));
-        const float y = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 + i));
-        v[BITS == 4 ? 2 * i : i] = scale * (x - z);
-        v[BITS == 4 ? 2 * i + 1 : 4 + i] = scale * (y - z);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = __byte_perm(i < 2 ? lo : hi, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+            const __half2 y = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), z2), s2);
+            o[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+        auto twice = [](float x) { return f32x2(__float_as_uint(x), __float_as_uint(x)); };
+        const float scale = __half2float(hs), zero = __half2float(hz);
+        const uint64_t s2 = twice(scale);
+        const uint64_t z2 = twice(BITS == 4 ? -scale * (128.0f + zero) : -(8388608.0f + zero));
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            uint64_t y = z2;
+            if (BITS == 4) {
+                const int sel = 0x7044 + (i / 2 << 8);
+                fma_f32x2(y, f32x2(__byte_perm(even, 0x43000000u, sel),
+                                   __byte_perm(odd, 0x43000000u, sel)), s2);
+            } else {
+                const uint32_t word = i < 4 ? w.x : w.y;
+                const int b = i & 2;           // the pair's first byte
+                fma_f32x2(y, f32x2(__byte_perm(word, 0x4B000000u, 0x7440 + b),
+                                   __byte_perm(word, 0x4B000000u, 0x7441 + b)), twice(1.0f));
+                const uint64_t d = y;
+                y = 0;
+                fma_f32x2(y, d, s2);
+            }
+            v[i] = f32x2_get(y, 0);
+            v[i + 1] = f32x2_get(y, 1);
+        }
+        kv_store8(at, v, wide);
     }
 }
 
-// Read back. A warp takes `rows` (1 to 32) consecutive tokens: lane i finds token i's sequence,
-// page and slot, and the warp then runs over the tokens' chunks, U passes of loads at a time. Of few and wide
-// tokens the warps of a CTA share each (1 << log_parts of them).
+// Read back. A CTA takes consecutive tokens: 1 << log_parts warps share each, and a warp has every
+// `apart`-th one, `rows` (1 to 32) of them. Lane i finds the warp's token i's sequence, page and
+// slot, and the warp then runs over the tokens' chunks, U passes of loads at a time.
+// The order of the writes decides the rest: 16384 x 32 x 128, 4 bits, bf16, took 70 us with four
+// passes and 32 or fewer consecutive tokens per warp, 64 with eight passes, 60 with all warps
+// writing side by side. (With 9 instructions per value instead of 7 it took the same.)
 template <typename T, int BITS, int U>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, int page_size,
                                                              int64_t n_pages,
@@ -351,21 +400,24 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
                                                              int n_seqs, int max_pages,
                                                              const int32_t* __restrict__ cu,
                                                              int64_t total, int rows, int log_parts,
-                                                             T* __restrict__ K, T* __restrict__ V) {
+                                                             T* __restrict__ K, T* __restrict__ V,
+                                                             int wide) {
     constexpr int H = U > 1 ? U / 2 : 1;       // passes of the keys, then of the values
     constexpr int64_t kNobody = -2, kMissing = -1;
     pdl_wait();
     const int lane = lane_id();
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x) >> 5;
-    const int parts = 1 << log_parts;          // warps of a token, all of one CTA
-    const int64_t step = static_cast<int64_t>(gridDim.x) * ((kKvThreads / 32) >> log_parts) * rows;
-    const int first_chunk = static_cast<int>(warp & (parts - 1)) * 32 * H;
-    for (int64_t t0 = (warp >> log_parts) * rows; t0 < total; t0 += step) {
+    const int parts = 1 << log_parts;                        // warps of a token
+    const int apart = (kKvThreads / 32) >> log_parts;        // tokens between a warp's
+    const int first_chunk = (warp_id() & (parts - 1)) * 32 * H;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * apart * rows;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * apart * rows + (warp_id() >> log_parts);
+         t0 < total; t0 += step) {
+        const int64_t t = t0 + lane * apart;                 // the token that the lane looks up
         int64_t mine = kNobody;
-        if (lane < rows && t0 + lane < total) {
-            const int b = kv_find_seq(cu, n_seqs, t0 + lane);
+        if (lane < rows && t < total) {
+            const int b = kv_find_seq(cu, n_seqs, t);
             if (b >= 0 && b < n_seqs) {        // else a row of no sequence: left as it was
-                const int64_t pos = t0 + lane - __ldg(cu + b);
+                const int64_t pos = t - __ldg(cu + b);
                 mine = kMissing;
                 if (pos >= 0) {
                     const unsigned pi = static_cast<unsigned>(pos) / static_cast<unsigned>(page_size);
@@ -378,7 +430,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
                 if (mine == kMissing) set_status(p.status, GPTQ_ERR_ARG);
             }
         }
-        const int n_tok = static_cast<int>(min(static_cast<int64_t>(rows), total - t0));
+        const int n_tok =
+            static_cast<int>(min(static_cast<int64_t>(rows), (total - t0 + apart - 1) >> (2 - log_parts)));
         const int n_rows = U > 1 ? n_tok : 2 * n_tok;   // tokens, or plane rows
         int r = 0, wc = first_chunk + lane;    // the lane's row and chunk
         for (int base = first_chunk; base < n_rows * p.wc; base += parts * 32 * H) {
@@ -407,14 +460,12 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvParams p, i
                         zb[u] = __ldg(p.zeros + g);
                     }
                 }
-                const int64_t out = (t0 + tok) * p.width + 8 * wc;
+                const int64_t out = (t0 + tok * apart) * p.width + 8 * wc;
                 T* first = (U == 1 && (r & 1) ? V : K) + out;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    float v[8];
-                    kv_values<BITS>(w[u], __half2float(__ushort_as_half(sb[u])),
-                                    __half2float(__ushort_as_half(zb[u])), v);
-                    kv_store8((u < H ? first : V + out) + 256 * (u % H), v);
+                    kv_values<T, BITS>(w[u], sb[u], zb[u], (u < H ? first : V + out) + 256 * (u % H),
+                                       wide);
                 }
             }
             wc += parts * 32 * H;
@@ -457,15 +508,17 @@ static gptq_status kv_write_launch(const void* K, const void* V, int64_t n, int6
 #define KV_WRITE(U)                                                             \
     (bits == 4 ? kv_write_group<T, 4, U>(k, v, n, ks, vs, slots, p, s) \
                : kv_write_group<T, 8, U>(k, v, n, ks, vs, slots, p, s))
-    // Eight passes where a group's lanes are as many (64 elements), and only as many as leave 16
-    // units for every SM: 64 tokens x 32 x 128 take 6.1 us with eight passes and 4.2 with two, 256
-    // tokens 6.2 with four and 5.2 with two, 16384 tokens 64 with eight, 7@ with four.
-    const int64_t units2 = n * p.wc / 32, enough = static_cast<int64_t>(num_sms()) * 16;
-    if (p.wc % 128 == 0 && p.tpg_shift >= 3 && units2 >= 4 * enough) return KV_WRITE(8);
-    if (p.wc % 64 == 0 && units2 >= 2 * enough) return KV_WRITE(4);
+    // 16384 x 32 x 128 in bf16 takes 62 us with eight passes, 72 with four, 105 with two (groups of
+    // 16: 85, 88, 103); a few tokens take the same with any.
+    if (p.wc % 128 == 0) return KV_WRITE(8);
+    if (p.wc % 64 == 0) return KV_WRITE(4);
     if (p.wc % 32 == 0) return KV_WRITE(2);
     return KV_WRITE(1);
 #undef KV_WRITE
+}
+
+static bool kv_aligned(const void* p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
 template <typename T>
@@ -473,38 +526,35 @@ static gptq_status kv_read_launch(const KvParams& p, int page_size, int64_t n_pa
                                   const int32_t* table, int n_seqs, int max_pages,
                                   const int32_t* cu, int64_t total, void* K, void* V, int bits,
                                   cudaStream_t s) {
-    // tokens per warp: up to 32, so that a search is shared, but fewer while warps are scarce
+    // Up to four warps take a token's passes in turn, and a warp takes as many tokens as make 8 KB,
+    // sharing the search, so that all CTAs together write one stretch of memory after the other.
+    // 16384 x 32 x 128, 8 bits: 66 us with one token per warp, 67 with two, 83 with 32 (65 and 80
+    // with a warp per token); 131072 tokens x 4 x 128, 1000 sequences: 81, 66, 79, with four 64.
+    int log_parts = 0;
+    while (log_parts < 2 && (128 << log_parts) < p.wc) ++log_parts;
+    const int64_t bytes = 2 * static_cast<int64_t>(p.width) * static_cast<int64_t>(sizeof(T));
     const int64_t warps = static_cast<int64_t>(num_sms()) * 32;
     int rows = 1;
-    while (rows < 32 && 2 * rows * warps <= total) rows *= 2;
-    // where tokens are scarcer still, two or four warps take a wide token's passes in turn (101
-    // tokens x 32 x 128 take 3.2 us so, 4.2 with two warps and 5.2 with one)
-    int log_parts = 0;
-    while (log_parts < 2 && (2 * total << log_parts) <= warps && (128 << log_parts) < p.wc)
-        ++log_parts;
+    while (rows < 32 && 2 * rows * bytes <= 8192 && 2 * rows * warps <= total << log_parts) rows *= 2;
     const int64_t per_cta = rows * ((kKvThreads / 32) >> log_parts);
     const int64_t want = (total + per_cta - 1) / per_cta;
     const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 64));
     T* k = static_cast<T*>(K);
     T* v = static_cast<T*>(V);
 #define KV_READ(U) (bits == 4 ? kv_read_kernel<T, 4, U> : kv_read_kernel<T, 8, U>)
-    // As many bytes in flight as pay: 16384 x 32 x 128 in bf16 takes 64 us with eight passes and 70
-    // with four at 4 bits, 80 and 74 at 8; 16384 x 8 x 128 in fp32 (which writes twice as much per
-    // chunk) 40 us with eight or four and 36 with two.
-    const bool half = sizeof(T) == 2;
-    auto* kernel = p.wc % 128 == 0 && bits == 4 && half ? KV_READ(8)
-                   : p.wc % 64 == 0 && half             ? KV_READ(4)
-                   : p.wc % 32 == 0                     ? KV_READ(2)
-                                                        : KV_READ(1);
+    // eight passes at a time while warps are scarce (512 tokens x 32 x 128, 4 bits: 4.2 us, 5.2 with
+    // four), else four (131072 x 8 x 128, 4 bits: 114 us, 118 with eight, 125 with two)
+    const bool few = (total << log_parts) <= 2 * warps;
+    auto* kernel = p.wc % 128 == 0 && few ? KV_READ(8)
+                   : p.wc % 64 == 0       ? KV_READ(4)
+                   : p.wc % 32 == 0       ? KV_READ(2)
+                                          : KV_READ(1);
 #undef KV_READ
     GPTQ_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kKvThreads), 0, s, p, page_size, n_pages, table,
-                             n_seqs, max_pages, cu, total, rows, log_parts, k, v));
+                             n_seqs, max_pages, cu, total, rows, log_parts, k, v,
+                             kv_aligned(K, 32) && kv_aligned(V, 32) ? 1 : 0));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
-}
-
-static bool kv_aligned(const void* p, uintptr_t a) {
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
 // the checks and the row geometry that writing and reading share

@@ -124,6 +124,64 @@ def test_read_matches_the_oracle(cuda_lib, H, D, bits, g, page, dtype):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("H,D,bits,g", [
+    (32, 128, 4, 64), (8, 128, 8, 128), (4, 256, 4, 32), (4, 128, 8, 64), (2, 128, 4, 16),
+    (1, 128, 8, 32), (3, 80, 4, 16), (7, 160, 8, 32)])
+def test_a_long_read_is_many_short_ones(cuda_lib, H, D, bits, g, dtype):
+    """Thousands of ragged tokens in one call give bit for bit what a call per sequence gives, and
+    those are checked against the oracle above; one sequence against the oracle here too. Rows
+    before the first sequence and behind the last stay as they were."""
+    page, rng = 16, np.random.default_rng(H + D)
+    lens = rng.integers(0, 1200, 40)
+    lens[3], lens[11] = 0, 1
+    first, extra = 5, 9
+    cu = (first + np.concatenate([[0], np.cumsum(lens)])).astype(np.int32)
+    total = int(cu[-1]) + extra
+    n_pages = int(sum(-(-x // page) for x in lens)) + 1
+    dev, host = _filled(cuda_lib, n_pages, page, H, D, bits, g, seed=D)
+    ids = rng.permutation(n_pages)
+    table = np.full((len(lens), 75), -1, np.int32)
+    at = 0
+    for b, x in enumerate(lens):
+        k = -(-int(x) // page)
+        table[b, :k] = ids[at:at + k]
+        at += k
+    K = torch.full((total, H, D), 7.0, dtype=dtype, device="cuda")
+    V = torch.full((total, H, D), -7.0, dtype=dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    td = torch.from_numpy(table).cuda()
+    cuda_lib.kv_cache_read(*dev, td, torch.from_numpy(cu).cuda(), total, bits=bits, dtype=dtype,
+                           out=(K, V), status=status)
+    for b, x in enumerate(lens):
+        one = torch.tensor([0, int(x)], dtype=torch.int32, device="cuda")
+        k, v = cuda_lib.kv_cache_read(*dev, td[b:b + 1], one, int(x), bits=bits, dtype=dtype)
+        assert torch.equal(K[cu[b]:cu[b + 1]], k) and torch.equal(V[cu[b]:cu[b + 1]], v), b
+    assert bool((K[:first] == 7).all()) and bool((K[cu[-1]:] == 7).all())
+    assert bool((V[:first] == -7).all()) and bool((V[cu[-1]:] == -7).all())
+    rk, rv = okv.read(*host, table[5:6], np.array([0, lens[5]]), bits)
+    _same(_np(K[cu[5]:cu[6]]), _rounded(rk, dtype))
+    _same(_np(V[cu[5]:cu[6]]), _rounded(rv, dtype))
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_read_into_rows_at_any_16_bytes(cuda_lib, dtype):
+    """Outputs that start 16 bytes behind a 32-byte boundary get the same values."""
+    H, D, bits, g, page, n = 4, 128, 8, 64, 16, 333
+    dev, _ = _filled(cuda_lib, 21, page, H, D, bits, g, seed=1)
+    table = torch.randperm(21, generator=torch.Generator().manual_seed(2)).int().view(1, -1).cuda()
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    ref = cuda_lib.kv_cache_read(*dev, table, cu, n, bits=bits, dtype=dtype)
+    skip = 16 // ref[0].element_size()
+    flat = torch.zeros(2, n * H * D + 2 * skip, dtype=dtype, device="cuda")
+    out = tuple(x[skip:skip + n * H * D].view(n, H, D) for x in flat)
+    assert all(x.data_ptr() % 16 == 0 for x in out) and out[0].data_ptr() % 32 == 16
+    cuda_lib.kv_cache_read(*dev, table, cu, n, bits=bits, out=out)
+    for a, b, x in zip(out, ref, flat):
+        assert torch.equal(a, b) and not bool(x[:skip].any()) and not bool(x[-skip:].any())
+
+
 @pytest.mark.parametrize("n_seqs", [1, 2, 31, 32, 33, 64, 1000, 1025, 2500])
 def test_read_finds_every_sequence(cuda_lib, n_seqs):
     """Rows of many sequences, some empty: each row comes from its own sequence's page."""
