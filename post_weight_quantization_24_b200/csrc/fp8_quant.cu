@@ -9,7 +9,7 @@
 //
 // Both kernels read X once into registers and write its codes from there: bytes per value are
 // the input's 2 or 4 plus 1, plus the scales. They are bound by HBM: 16384 x 11008 bf16 activations
-// take 93 us (5.9 TB/s), 11008 x 4096 fp16 weights 21 us (6.3 TB/s), 4100 x 5136 fp32 weights 17
+// take 82 us (6.6 TB/s), 11008 x 4096 fp16 weights 21 us (6.3 TB/s), 4100 x 5136 fp32 weights 17
 // us (6.1 TB/s); a copy runs at 6.55 TB/s.
 #include <algorithm>
 
@@ -37,16 +37,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return o;
 }
 
-// one 16-byte vector's codes: 8 bytes (fp16, bf16) or 4 (fp32)
+// one 16-byte vector's codes: two words (fp16, bf16) or one (fp32)
 template <typename T>
-__device__ __forceinline__ void store_codes_vec(uint8_t* p, const uint4& u, float r) {
+__device__ __forceinline__ void codes_vec(const uint4& u, float r, uint32_t* w) {
     float v[Vec<T>::N];
     Vec<T>::unpack(u, v);
-    uint32_t w[Vec<T>::N / 4];
 #pragma unroll
     for (int i = 0; i < Vec<T>::N / 4; ++i)
         w[i] = e4m3x2(v[4 * i] * r, v[4 * i + 1] * r) |
                (e4m3x2(v[4 * i + 2] * r, v[4 * i + 3] * r) << 16);
+}
+template <typename T>
+__device__ __forceinline__ void store_codes_vec(uint8_t* p, const uint4& u, float r) {
+    uint32_t w[2];
+    codes_vec<T>(u, r, w);
     if constexpr (Vec<T>::N == 8)
         *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else
@@ -62,16 +66,29 @@ __device__ __forceinline__ uint32_t amax_vec(const uint4& u, uint32_t m) {
     return m;
 }
 
-// A CTA takes 8 tokens x 1024 channels. A warp takes one token: 8 lanes per 128-channel block, 4
-// blocks per pass, 2 passes, all loads first; a lane's vectors lie 8 vectors apart, so that every
-// load and store of 8 lanes is one contiguous run (a pass of fp16 is 1 KB of one row). The scales
-// leave through shared memory as runs of 8 tokens. (With 4 tokens x 128 channels per warp, 256 bytes
-// of a row at a time, and plain loads it took 101 us instead of 93.)
-template <typename T>
+// 32 bytes at once where they start on such a boundary, else as two halves.
+__device__ __forceinline__ void load32(const void* p, int wide, uint4* x) {
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x),
+                       "=r"(x[1].y), "=r"(x[1].z), "=r"(x[1].w)
+                     : "l"(p));
+    } else {
+        x[0] = __ldcs(static_cast<const uint4*>(p));
+        x[1] = __ldcs(static_cast<const uint4*>(p) + 1);
+    }
+}
+
+// A CTA takes 8 tokens x 512 P channels. A warp takes one token: 8 lanes per 128-channel block, 16
+// consecutive values per lane (one store of 16 codes), 4 blocks per pass, P passes, all loads
+// first. The scales leave through shared memory as runs of 8 tokens. 16384 x 11008 bf16 takes 82 us
+// with P = 4, 86 with 2, 100 with 1; 94 with P = 2 and a lane's two vectors 128 bytes apart (8-byte
+// stores); 101 with 4 tokens x 128 channels per warp.
+template <typename T, int P>
 __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, int64_t n, int d,
                                                       uint8_t* __restrict__ codes,
-                                                      float* __restrict__ scales) {
-    constexpr int N = Vec<T>::N, C = 128 / (8 * N), P = 2;
+                                                      float* __restrict__ scales, int wide) {
+    constexpr int N = Vec<T>::N, C = 16 / N;             // vectors of a lane and block
     __shared__ float sc[4 * P][8];
     pdl_wait();
     const int lane = lane_id(), part = lane & 7;
@@ -82,13 +99,15 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
     const int64_t t = rb * 8 + warp_id();
     uint4 x[P][C];
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p) {
+        const int k = (b0 + 4 * p) * 128 + part * 16;    // d is a multiple of 16
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = (b0 + 4 * p) * 128 + (c * 8 + part) * N;
-            x[p][c] = make_uint4(0, 0, 0, 0);
-            if (t < n && k < d) x[p][c] = __ldcs(reinterpret_cast<const uint4*>(X + t * d + k));
+        for (int c = 0; c < C; ++c) x[p][c] = make_uint4(0, 0, 0, 0);
+        if (t < n && k < d) {
+#pragma unroll
+            for (int c = 0; c < C; c += 2) load32(X + t * d + k + c * N, wide, &x[p][c]);
         }
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         uint32_t m = 0;
@@ -97,12 +116,12 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const Fp8Scale f = fp8_scale(m);
-        if (t < n) {
+        const int k = (b0 + 4 * p) * 128 + part * 16;
+        if (t < n && k < d) {
+            uint32_t w[4];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int k = (b0 + 4 * p) * 128 + (c * 8 + part) * N;
-                if (k < d) store_codes_vec<T>(codes + t * d + k, x[p][c], f.r);
-            }
+            for (int c = 0; c < C; ++c) codes_vec<T>(x[p][c], f.r, w + c * (N / 4));
+            *reinterpret_cast<uint4*>(codes + t * d + k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         if (part == 0) sc[4 * p + (lane >> 3)][warp_id()] = f.s;
     }
@@ -163,15 +182,29 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp8_weight_kernel
     if (threadIdx.x == 0) scales[blockIdx.x] = f.s;
 }
 
+template <typename T, int P>
+static gptq_status fp8_act_go(const void* X, int64_t n, int d, uint8_t* codes, float* scales,
+                              int64_t ctas, cudaStream_t s) {
+    if (ctas > 0x7FFFFFFF) return GPTQ_ERR_ARG;
+    const int wide = (reinterpret_cast<uintptr_t>(X) & 31) == 0;
+    GPTQ_CUDA_TRY(launch_pdl(fp8_act_kernel<T, P>, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s,
+                             static_cast<const T*>(X), n, d, codes, scales, wide));
+    GPTQ_LAUNCHED();
+    return GPTQ_OK;
+}
+
+// Passes per CTA: 2 KB of a row at a time in 16 bits, 4 KB where that leaves 16 CTAs for every SM
+// (16384 x 4096 fp16: 31.8 us, 32.9 with 2 KB; 2048 x 4096: 6.5 and 5.9), 1 KB where 2 KB leave fewer
+// than 4 (513 x 5136: 3.1 us, 3.3 with 2 KB). In fp32 no more than 4 KB (16384 x 11008: 129 us with
+// 2 KB or 4 KB, 137 with 8 KB).
 template <typename T>
 static gptq_status fp8_act_launch(const void* X, int64_t n, int d, uint8_t* codes, float* scales,
                                   cudaStream_t s) {
-    const int64_t ctas = ((n + 7) / 8) * ((d + 1023) / 1024);
-    if (ctas > 0x7FFFFFFF) return GPTQ_ERR_ARG;
-    GPTQ_CUDA_TRY(launch_pdl(fp8_act_kernel<T>, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, s,
-                             static_cast<const T*>(X), n, d, codes, scales));
-    GPTQ_LAUNCHED();
-    return GPTQ_OK;
+    auto ctas = [&](int p) { return ((n + 7) / 8) * ((d + 512 * p - 1) / (512 * p)); };
+    if (sizeof(T) == 2 && ctas(4) >= 16 * num_sms())
+        return fp8_act_go<T, 4>(X, n, d, codes, scales, ctas(4), s);
+    if (ctas(2) >= 4 * num_sms()) return fp8_act_go<T, 2>(X, n, d, codes, scales, ctas(2), s);
+    return fp8_act_go<T, 1>(X, n, d, codes, scales, ctas(1), s);
 }
 
 template <typename T>

@@ -98,6 +98,42 @@ def test_quantizers_write_only_their_outputs(cuda_lib):
     assert bool((sbuf[0] == -7).all()) and bool((sbuf[4] == -7).all())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("n,d", [(9, 1040), (3, 272), (1, 16)])
+def test_quantize_act_of_rows_at_any_16_bytes(cuda_lib, n, d, dtype):
+    """Inputs that start 16 bytes behind a 32-byte boundary get the same codes and scales."""
+    x = _values(n, d, seed=n, dtype=dtype).cuda()
+    skip = 16 // x.element_size()
+    buf = torch.empty(n * d + 2 * skip, dtype=dtype, device="cuda")
+    y = buf[skip:skip + n * d].view(n, d)
+    y.copy_(x)
+    assert y.data_ptr() % 32 == 16 and x.data_ptr() % 32 == 0
+    a, b = cuda_lib.fp8_quantize_act(x), cuda_lib.fp8_quantize_act(y)
+    assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("n,d", [(8200, 4112), (1500, 5136), (5, 8208)])
+def test_quantize_act_of_many_tokens_is_that_of_few(cuda_lib, n, d, dtype):
+    """Every row's codes and scales are those of a call with a few rows, which are checked against
+    the oracle above (a few here too)."""
+    x = torch.randn(n, d, generator=torch.Generator(device="cuda").manual_seed(d), device="cuda")
+    x = (x * torch.exp(torch.randn(d, generator=torch.Generator().manual_seed(n)).cuda())).to(dtype)
+    x[n // 2, 17], x[n - 1, d - 1] = float("nan"), float("inf")
+    codes, scales = cuda_lib.fp8_quantize_act(x)
+    for r0 in (0, n // 2 - 2, n - 5):
+        c, s = cuda_lib.fp8_quantize_act(x[r0:r0 + 5])
+        assert torch.equal(c.view(torch.uint8), codes[r0:r0 + 5].view(torch.uint8))
+        assert torch.equal(s.view(torch.int32), scales[:, r0:r0 + 5].contiguous().view(torch.int32))
+        rc, rs = ofp8.quantize_act(_np(x[r0:r0 + 5]))
+        _same(_np(c), rc)
+        _same(_np(s), rs.astype(np.float64))
+    step = max(1, n // 64)
+    c, s = cuda_lib.fp8_quantize_act(x[::step].contiguous())
+    assert torch.equal(c.view(torch.uint8), codes[::step].view(torch.uint8))
+    assert torch.equal(s.view(torch.int32), scales[:, ::step].contiguous().view(torch.int32))
+
+
 def _quantized(n, d_in, d_out, seed):
     xc, xs = ofp8.quantize_act(_np(_values(n, d_in, seed)))
     wc, ws = ofp8.quantize_weight(_np(_values(d_out, d_in, seed + 1, spread=0.3)))
