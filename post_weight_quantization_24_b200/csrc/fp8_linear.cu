@@ -15,8 +15,8 @@
 //                      TMA and MMAs alone take 0.61 ms; without the promotion's multiply-adds
 //                      0.71 ms.
 //   fp8_stream_kernel  128 channels x 16 to 128 tokens per CTA, the input channels split over a
-//                      cluster: for all other calls. 1 token, 4096 -> 4096: 7.4 us; 37 tokens,
-//                      11008 -> 4096, bf16 with residual: 15.2 us, 4 to 5 us of them fixed
+//                      cluster: for all other calls. 1 token, 4096 -> 4096: 7.2 us; 37 tokens,
+//                      11008 -> 4096, bf16 with residual: 15.5 us, about 4 us of them fixed
 //                      (set-up, first loads, the join) and the rest at 4 to 5 TB/s of weights.
 #include <algorithm>
 #include <atomic>
