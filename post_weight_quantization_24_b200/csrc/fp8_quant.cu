@@ -37,24 +37,21 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return o;
 }
 
-// one 16-byte vector's codes: two words (fp16, bf16) or one (fp32)
+// 16 values' codes, one 16-byte store
 template <typename T>
-__device__ __forceinline__ void codes_vec(const uint4& u, float r, uint32_t* w) {
-    float v[Vec<T>::N];
-    Vec<T>::unpack(u, v);
+__device__ __forceinline__ void store_codes16(uint8_t* p, const uint4* x, float r) {
+    constexpr int N = Vec<T>::N;
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N / 4; ++i)
-        w[i] = e4m3x2(v[4 * i] * r, v[4 * i + 1] * r) |
-               (e4m3x2(v[4 * i + 2] * r, v[4 * i + 3] * r) << 16);
-}
-template <typename T>
-__device__ __forceinline__ void store_codes_vec(uint8_t* p, const uint4& u, float r) {
-    uint32_t w[2];
-    codes_vec<T>(u, r, w);
-    if constexpr (Vec<T>::N == 8)
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else
-        *reinterpret_cast<uint32_t*>(p) = w[0];
+    for (int c = 0; c < 16 / N; ++c) {
+        float v[N];
+        Vec<T>::unpack(x[c], v);
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            w[(c * N + i) / 4] = e4m3x2(v[i] * r, v[i + 1] * r) |
+                                 (e4m3x2(v[i + 2] * r, v[i + 3] * r) << 16);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T>
@@ -117,12 +114,7 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
         for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const Fp8Scale f = fp8_scale(m);
         const int k = (b0 + 4 * p) * 128 + part * 16;
-        if (t < n && k < d) {
-            uint32_t w[4];
-#pragma unroll
-            for (int c = 0; c < C; ++c) codes_vec<T>(x[p][c], f.r, w + c * (N / 4));
-            *reinterpret_cast<uint4*>(codes + t * d + k) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        if (t < n && k < d) store_codes16<T>(codes + t * d + k, x[p], f.r);
         if (part == 0) sc[4 * p + (lane >> 3)][warp_id()] = f.s;
     }
     __syncthreads();
@@ -134,30 +126,31 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
 }
 
 // A CTA of 256 threads takes one 128 x 128 block, all of it in flight at once (32 KB of fp16): 8
-// lanes per row, 4 rows per warp and step. Registers are bounded for three CTAs per SM with 16-bit
-// inputs (with that, streaming loads and the overlapped launch 26.5 us became 21).
+// lanes per row with 16 consecutive values each, 4 rows per warp and step. Registers are bounded
+// for three CTAs per SM with 16-bit inputs (with that, streaming loads and the overlapped launch
+// 26.5 us became 21).
 template <typename T>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp8_weight_kernel(const T* __restrict__ W, int d_out,
-                                                         int d_in, uint8_t* __restrict__ codes,
-                                                         float* __restrict__ scales) {
-    constexpr int N = Vec<T>::N, C = 128 / (8 * N);
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
+    fp8_weight_kernel(const T* __restrict__ W, int d_out, int d_in, uint8_t* __restrict__ codes,
+                      float* __restrict__ scales, int wide) {
+    constexpr int N = Vec<T>::N, C = 16 / N;
     __shared__ uint32_t warp_max[8];
     pdl_wait();
-    const int lane = lane_id(), part = lane & 7;
+    const int lane = lane_id();
     const int nb = (d_in + 127) / 128;
     const int64_t rb = blockIdx.x / nb;
     const int b = static_cast<int>(blockIdx.x - rb * nb);
+    const int k = b * 128 + (lane & 7) * 16;             // d_in is a multiple of 16
     uint4 x[4][C];
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int64_t row = rb * 128 + j * 32 + warp_id() * 4 + (lane >> 3);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = b * 128 + (c * 8 + part) * N;
-            x[j][c] = make_uint4(0, 0, 0, 0);
-            if (row < d_out && k < d_in)
-                x[j][c] = __ldcs(reinterpret_cast<const uint4*>(W + row * d_in + k));
+        for (int c = 0; c < C; ++c) x[j][c] = make_uint4(0, 0, 0, 0);
+        if (row < d_out && k < d_in) {
+#pragma unroll
+            for (int c = 0; c < C; c += 2) load32(W + row * d_in + k + c * N, wide, &x[j][c]);
         }
     }
 #pragma unroll
@@ -173,11 +166,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp8_weight_kernel
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int64_t row = rb * 128 + j * 32 + warp_id() * 4 + (lane >> 3);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int k = b * 128 + (c * 8 + part) * N;
-            if (row < d_out && k < d_in) store_codes_vec<T>(codes + row * d_in + k, x[j][c], f.r);
-        }
+        if (row < d_out && k < d_in) store_codes16<T>(codes + row * d_in + k, x[j], f.r);
     }
     if (threadIdx.x == 0) scales[blockIdx.x] = f.s;
 }
@@ -214,7 +203,8 @@ static gptq_status fp8_weight_launch(const void* W, int d_out, int d_in, uint8_t
     const int64_t blocks = ((static_cast<int64_t>(d_out) + 127) / 128) * ((d_in + 127) / 128);
     if (blocks > 0x7FFFFFFF) return GPTQ_ERR_ARG;
     GPTQ_CUDA_TRY(launch_pdl(fp8_weight_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                             s, static_cast<const T*>(W), d_out, d_in, codes, scales));
+                             s, static_cast<const T*>(W), d_out, d_in, codes, scales,
+                             (reinterpret_cast<uintptr_t>(W) & 31) == 0 ? 1 : 0));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }

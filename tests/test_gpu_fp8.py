@@ -100,7 +100,7 @@ def test_quantizers_write_only_their_outputs(cuda_lib):
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("n,d", [(9, 1040), (3, 272), (1, 16)])
-def test_quantize_act_of_rows_at_any_16_bytes(cuda_lib, n, d, dtype):
+def test_quantize_rows_at_any_16_bytes(cuda_lib, n, d, dtype):
     """Inputs that start 16 bytes behind a 32-byte boundary get the same codes and scales."""
     x = _values(n, d, seed=n, dtype=dtype).cuda()
     skip = 16 // x.element_size()
@@ -108,8 +108,10 @@ def test_quantize_act_of_rows_at_any_16_bytes(cuda_lib, n, d, dtype):
     y = buf[skip:skip + n * d].view(n, d)
     y.copy_(x)
     assert y.data_ptr() % 32 == 16 and x.data_ptr() % 32 == 0
-    a, b = cuda_lib.fp8_quantize_act(x), cuda_lib.fp8_quantize_act(y)
-    assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+    for f in (cuda_lib.fp8_quantize_act, cuda_lib.fp8_quantize_weight):
+        a, b = f(x), f(y)
+        assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8))
+        assert torch.equal(a[1], b[1])
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
