@@ -4,8 +4,9 @@ infrastructure only).
 e4m3 has 1 sign, 4 exponent (bias 7) and 3 fraction bits, no infinities, NaN as exponent and
 fraction all ones; its finite magnitudes end at 448 and its subnormal step is 2^-9.
 
-A block's scale and codes: a = max(max|x|, 2^-100), s = fl32(a/448), r = fl32(448/a), and each
-code is the e4m3 value nearest to fl32(x·r), halves to even (at most 448). A block that holds a
+A block's scale and codes: a = max(max|x|, 2^-100), s = fl32(a/448), and each code is the e4m3
+value nearest to x·448/a, halves to even (the fp64 quotient of fp32 values is never rounded onto
+a tie or off one: it is one or at least 2^-30 of itself away). A block that holds a
 NaN or an infinity has s = NaN and NaN codes. Blocks are 1 x 128 (activations) or 128 x 128
 (weights), cut off at the matrix's edges.
 
@@ -39,8 +40,7 @@ def quantize(x, rows):
                 continue
             a = np.float32(max(np.max(np.abs(blk)), 2.0 ** -100))
             scales[i, b] = a / np.float32(448.0)
-            with np.errstate(under="ignore"):
-                codes[at] = e4m3_round(blk.astype(np.float32) * (np.float32(448.0) / a))
+            codes[at] = e4m3_round(blk * 448.0 / np.float64(a))
     return codes, scales
 
 

@@ -1,9 +1,10 @@
 // e4m3 codes with one fp32 scale per block of 128: activations per token and 128 channels,
 // weights per 128 x 128 block.
 //
-// a = max(max|x|, 2^-100), s = a/448, r = 448/a, code = e4m3(x*r). 448 is e4m3's largest
-// magnitude, so the block's largest value lands on the top code; the floor keeps s and r normal
-// fp32 numbers for every input (an all-zero block gets s = 2^-100/448 and zero codes).
+// a = max(max|x|, 2^-100), s = a/448, code = the e4m3 value nearest to x*448/a (exactly, halves to
+// even). 448 is e4m3's largest magnitude, so the block's largest value lands on the top code; the
+// floor keeps s and r = 448/a normal fp32 numbers for every input (an all-zero block gets s =
+// 2^-100/448 and zero codes).
 // max|x| is taken over integer magnitudes, which carries NaN and infinity along: such a block
 // gets s = r = NaN and NaN codes.
 //
@@ -20,14 +21,16 @@ namespace gq {
 
 constexpr float kE4m3Max = 448.0f;
 
+// a, s, and 448/a as r + r_lo
 struct Fp8Scale {
-    float s, r;
+    float a, s, r, r_lo;
 };
 
 __device__ __forceinline__ Fp8Scale fp8_scale(uint32_t amax_bits) {
     const float a = amax_bits >= kInfBits ? __uint_as_float(0x7FC00000u)
                                           : fmaxf(__uint_as_float(amax_bits), 0x1p-100f);
-    return {__fdiv_rn(a, kE4m3Max), __fdiv_rn(kE4m3Max, a)};
+    const float r = __fdiv_rn(kE4m3Max, a);
+    return {a, __fdiv_rn(a, kE4m3Max), r, __fdiv_rn(fmaf(-r, a, kE4m3Max), a)};
 }
 
 // two products to two e4m3 codes, the first in the low byte (|x*r| <= 448 up to a rounding)
@@ -37,9 +40,44 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return o;
 }
 
+// The exact decision for four fp32 values, out of line: the fp64 quotient (never rounded onto a
+// tie, from which it is at least 2^-30 of itself away) to fp32 with the last bit telling whether
+// anything was cut off, to e4m3.
+static __device__ __noinline__ uint32_t codes_exact(float4 v, float a) {
+    float p[4];
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const double q = static_cast<double>(x[i]) * 448.0 / static_cast<double>(a);
+        const float f = __double2float_rz(q);
+        p[i] = __uint_as_float(__float_as_uint(f) | (static_cast<double>(f) != q ? 1u : 0u));
+    }
+    return e4m3x2(p[0], p[1]) | (e4m3x2(p[2], p[3]) << 16);
+}
+
+// Four values' codes.
+//   16-bit types: fma(v, r, v*r_lo) is the quotient within 2^-23 of itself, and the quotient itself
+//   where that is an fp32 number; with v and a of 11 bits it is a tie or 2^-17 off one.
+//   fp32: both ends of a bracket r (1 -+ 2^-22) (r and the products are within 2^-24) are rounded;
+//   where their codes differ (one value in 10^6) the exact decision is made.
+template <typename T>
+__device__ __forceinline__ uint32_t codes4(const float* v, const Fp8Scale& f) {
+    float p[4];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = fmaf(v[i], f.r, v[i] * f.r_lo);
+        return e4m3x2(p[0], p[1]) | (e4m3x2(p[2], p[3]) << 16);
+    } else {
+        const float up = f.r * (1.0f + 0x1p-22f), dn = f.r * (1.0f - 0x1p-22f);
+        const uint32_t w = e4m3x2(v[0] * up, v[1] * up) | (e4m3x2(v[2] * up, v[3] * up) << 16);
+        const uint32_t x = e4m3x2(v[0] * dn, v[1] * dn) | (e4m3x2(v[2] * dn, v[3] * dn) << 16);
+        return w == x ? w : codes_exact(make_float4(v[0], v[1], v[2], v[3]), f.a);
+    }
+}
+
 // 16 values' codes, one 16-byte store
 template <typename T>
-__device__ __forceinline__ void store_codes16(uint8_t* p, const uint4* x, float r) {
+__device__ __forceinline__ void store_codes16(uint8_t* p, const uint4* x, const Fp8Scale& f) {
     constexpr int N = Vec<T>::N;
     uint32_t w[4];
 #pragma unroll
@@ -47,9 +85,7 @@ __device__ __forceinline__ void store_codes16(uint8_t* p, const uint4* x, float 
         float v[N];
         Vec<T>::unpack(x[c], v);
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            w[(c * N + i) / 4] = e4m3x2(v[i] * r, v[i + 1] * r) |
-                                 (e4m3x2(v[i + 2] * r, v[i + 3] * r) << 16);
+        for (int i = 0; i < N; i += 4) w[(c * N + i) / 4] = codes4<T>(v + i, f);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -114,7 +150,7 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
         for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const Fp8Scale f = fp8_scale(m);
         const int k = (b0 + 4 * p) * 128 + part * 16;
-        if (t < n && k < d) store_codes16<T>(codes + t * d + k, x[p], f.r);
+        if (t < n && k < d) store_codes16<T>(codes + t * d + k, x[p], f);
         if (part == 0) sc[4 * p + (lane >> 3)][warp_id()] = f.s;
     }
     __syncthreads();
@@ -166,7 +202,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int64_t row = rb * 128 + j * 32 + warp_id() * 4 + (lane >> 3);
-        if (row < d_out && k < d_in) store_codes16<T>(codes + row * d_in + k, x[j], f.r);
+        if (row < d_out && k < d_in) store_codes16<T>(codes + row * d_in + k, x[j], f);
     }
     if (threadIdx.x == 0) scales[blockIdx.x] = f.s;
 }
