@@ -385,9 +385,9 @@ gptq_status gptq_silu_mul(const void* GU, int64_t n_tokens, int d_ff, void* A, v
  * channels, and their product with fp32 accumulation. It stands beside the W4A16 layer for
  * projections that keep 8 bits and have the tensor cores' 8-bit rate to win.
  *   e4m3: 4 exponent and 3 fraction bits, largest magnitude 448, no infinities, code 0x7F NaN.
- *   A block's scale and codes: a = max(max|x|, 2^-100), s = a / 448, r = 448 / a (both fp32
- *   divisions), code = e4m3(x * r): the fp32 product rounded to nearest, halves to even. A block
- *   that holds a NaN or an infinity gets s = NaN and NaN codes, so what is computed from it is NaN.
+ *   A block's scale and codes: a = max(max|x|, 2^-100), s = a / 448 (an fp32 division), code = the
+ *   e4m3 value nearest to x * 448 / a, halves to even (of the exact quotient). A block that holds
+ *   a NaN or an infinity gets s = NaN and NaN codes, so what is computed from it is NaN.
  * ------------------------------------------------------------------------------------------ */
 
 /* Codes and scales of activations.

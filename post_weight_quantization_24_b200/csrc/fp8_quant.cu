@@ -10,8 +10,8 @@
 //
 // Both kernels read X once into registers and write its codes from there: bytes per value are
 // the input's 2 or 4 plus 1, plus the scales. They are bound by HBM: 16384 x 11008 bf16 activations
-// take 82 us (6.6 TB/s), 11008 x 4096 fp16 weights 21 us (6.3 TB/s), 4100 x 5136 fp32 weights 17
-// us (6.1 TB/s); a copy runs at 6.55 TB/s.
+// take 88 us (6.2 TB/s), 11008 x 4096 fp16 weights 21 us (6.3 TB/s), 4100 x 5136 fp32 weights 19
+// us (5.4 TB/s; 17 with one rounding and no bracket); a copy runs at 6.55 TB/s.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -75,6 +75,17 @@ __device__ __forceinline__ uint32_t codes4(const float* v, const Fp8Scale& f) {
     }
 }
 
+// one 16-byte vector's codes: 8 bytes (fp16, bf16) or 4 (fp32)
+template <typename T>
+__device__ __forceinline__ void store_codes_vec(uint8_t* p, const uint4& u, const Fp8Scale& f) {
+    float v[Vec<T>::N];
+    Vec<T>::unpack(u, v);
+    if constexpr (Vec<T>::N == 8)
+        *reinterpret_cast<uint2*>(p) = make_uint2(codes4<T>(v, f), codes4<T>(v + 4, f));
+    else
+        *reinterpret_cast<uint32_t*>(p) = codes4<T>(v, f);
+}
+
 // 16 values' codes, one 16-byte store
 template <typename T>
 __device__ __forceinline__ void store_codes16(uint8_t* p, const uint4* x, const Fp8Scale& f) {
@@ -116,7 +127,8 @@ __device__ __forceinline__ void load32(const void* p, int wide, uint4* x) {
 // consecutive values per lane (one store of 16 codes), 4 blocks per pass, P passes, all loads
 // first. The scales leave through shared memory as runs of 8 tokens. 16384 x 11008 bf16 takes 82 us
 // with P = 4, 86 with 2, 100 with 1; 94 with P = 2 and a lane's two vectors 128 bytes apart (8-byte
-// stores); 101 with 4 tokens x 128 channels per warp.
+// stores); 101 with 4 tokens x 128 channels per warp. The second multiply-add that makes the codes
+// exact then cost 6 us (two values per instruction: 13).
 template <typename T, int P>
 __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, int64_t n, int d,
                                                       uint8_t* __restrict__ codes,
@@ -162,31 +174,31 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
 }
 
 // A CTA of 256 threads takes one 128 x 128 block, all of it in flight at once (32 KB of fp16): 8
-// lanes per row with 16 consecutive values each, 4 rows per warp and step. Registers are bounded
+// lanes per row, whose 16-byte vectors lie 8 apart, 4 rows per warp and step. Registers are bounded
 // for three CTAs per SM with 16-bit inputs (with that, streaming loads and the overlapped launch
-// 26.5 us became 21).
+// 26.5 us became 21; with 32-byte loads as above 24).
 template <typename T>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
     fp8_weight_kernel(const T* __restrict__ W, int d_out, int d_in, uint8_t* __restrict__ codes,
-                      float* __restrict__ scales, int wide) {
+                      float* __restrict__ scales) {
     constexpr int N = Vec<T>::N, C = 16 / N;
     __shared__ uint32_t warp_max[8];
     pdl_wait();
-    const int lane = lane_id();
+    const int lane = lane_id(), part = lane & 7;
     const int nb = (d_in + 127) / 128;
     const int64_t rb = blockIdx.x / nb;
     const int b = static_cast<int>(blockIdx.x - rb * nb);
-    const int k = b * 128 + (lane & 7) * 16;             // d_in is a multiple of 16
     uint4 x[4][C];
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int64_t row = rb * 128 + j * 32 + warp_id() * 4 + (lane >> 3);
 #pragma unroll
-        for (int c = 0; c < C; ++c) x[j][c] = make_uint4(0, 0, 0, 0);
-        if (row < d_out && k < d_in) {
-#pragma unroll
-            for (int c = 0; c < C; c += 2) load32(W + row * d_in + k + c * N, wide, &x[j][c]);
+        for (int c = 0; c < C; ++c) {
+            const int k = b * 128 + (c * 8 + part) * N;
+            x[j][c] = make_uint4(0, 0, 0, 0);
+            if (row < d_out && k < d_in)
+                x[j][c] = __ldcs(reinterpret_cast<const uint4*>(W + row * d_in + k));
         }
     }
 #pragma unroll
@@ -202,7 +214,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int64_t row = rb * 128 + j * 32 + warp_id() * 4 + (lane >> 3);
-        if (row < d_out && k < d_in) store_codes16<T>(codes + row * d_in + k, x[j], f);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = b * 128 + (c * 8 + part) * N;
+            if (row < d_out && k < d_in) store_codes_vec<T>(codes + row * d_in + k, x[j][c], f);
+        }
     }
     if (threadIdx.x == 0) scales[blockIdx.x] = f.s;
 }
@@ -220,8 +236,8 @@ static gptq_status fp8_act_go(const void* X, int64_t n, int d, uint8_t* codes, f
 
 // Passes per CTA: 2 KB of a row at a time in 16 bits, 4 KB where that leaves 16 CTAs for every SM
 // (16384 x 4096 fp16: 31.8 us, 32.9 with 2 KB; 2048 x 4096: 6.5 and 5.9), 1 KB where 2 KB leave fewer
-// than 4 (513 x 5136: 3.1 us, 3.3 with 2 KB). In fp32 no more than 4 KB (16384 x 11008: 129 us with
-// 2 KB or 4 KB, 137 with 8 KB).
+// than 4 (513 x 5136: 3.1 us, 3.3 with 2 KB). In fp32 no more than 4 KB (16384 x 11008: 8 KB took 6 % more).
+// The times are those before the codes were made exact.
 template <typename T>
 static gptq_status fp8_act_launch(const void* X, int64_t n, int d, uint8_t* codes, float* scales,
                                   cudaStream_t s) {
@@ -239,8 +255,7 @@ static gptq_status fp8_weight_launch(const void* W, int d_out, int d_in, uint8_t
     const int64_t blocks = ((static_cast<int64_t>(d_out) + 127) / 128) * ((d_in + 127) / 128);
     if (blocks > 0x7FFFFFFF) return GPTQ_ERR_ARG;
     GPTQ_CUDA_TRY(launch_pdl(fp8_weight_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                             s, static_cast<const T*>(W), d_out, d_in, codes, scales,
-                             (reinterpret_cast<uintptr_t>(W) & 31) == 0 ? 1 : 0));
+                             s, static_cast<const T*>(W), d_out, d_in, codes, scales));
     GPTQ_LAUNCHED();
     return GPTQ_OK;
 }
