@@ -396,7 +396,8 @@ gptq_status gptq_silu_mul(const void* GU, int64_t n_tokens, int d_ff, void* A, v
  *   codes    device uint8 [n_tokens x d] (e4m3), 16-byte aligned.
  *   scales   device fp32 [ceil(d/128) x n_tokens]: scales[b][t] of token t's channels 128b..128b+127
  *            (the last block may be narrower).
- * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+ * X, codes and scales may not overlap (GPTQ_ERR_ARG). Asynchronous. Errors: ARG, CUDA,
+ * UNSUPPORTED. */
 gptq_status fp8_quantize_act(const void* X, int x_dtype, int64_t n_tokens, int d, uint8_t* codes,
                              float* scales, void* stream);
 
@@ -405,7 +406,8 @@ gptq_status fp8_quantize_act(const void* X, int x_dtype, int64_t n_tokens, int d
  *            d_in: a multiple of 16, <= 65536.
  *   codes    device uint8 [d_out x d_in] (e4m3), 16-byte aligned.
  *   scales   device fp32 [ceil(d_out/128) x ceil(d_in/128)] (the last blocks may be smaller).
- * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+ * W, codes and scales may not overlap (GPTQ_ERR_ARG). Asynchronous. Errors: ARG, CUDA,
+ * UNSUPPORTED. */
 gptq_status fp8_quantize_weight(const void* W, int w_dtype, int d_out, int d_in, uint8_t* codes,
                                 float* scales, void* stream);
 
@@ -417,12 +419,12 @@ gptq_status fp8_quantize_weight(const void* W, int w_dtype, int d_out, int d_in,
  *   W8, w_scales   as fp8_quantize_weight writes them.   d_in: a multiple of 16, <= 65536.
  *                  d_out >= 1.
  *   R        device, Y's type, [n_tokens x d_out], or NULL (a residual added in fp32 before the
- *            rounding; may be the same buffer as Y).
+ *            rounding). R == Y is allowed, a partial overlap is not.
  *   Y        device [n_tokens x d_out], fp16, fp32 or bf16 (y_dtype).
  *            X8, W8, Y and R 16-byte aligned.
  *   status_dev device int or NULL: set to GPTQ_ERR_TIMEOUT if a bounded wait gave up.
- * Y may overlap no other argument but R. The order in which blocks are summed depends on the
- * sizes (n_tokens among them). Asynchronous, no workspace, may be captured; equal inputs give equal
+ * Y may overlap no argument, unless R == Y (GPTQ_ERR_ARG). The order in which blocks are summed
+ * depends on the sizes (n_tokens among them). Asynchronous, no workspace, may be captured; equal inputs give equal
  * bits. Errors: ARG, CUDA, UNSUPPORTED. */
 gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int64_t n_tokens, int d_in,
                        const uint8_t* W8, const float* w_scales, int d_out, const void* R, void* Y,
@@ -455,7 +457,8 @@ gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int64_t n_token
  *   n_slots  n_pages * page_size of the cache.
  *   status_dev device int or NULL: set to GPTQ_ERR_ARG if a slot is >= n_slots (that token is
  *            skipped).
- * Only the named slots change. Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+ * Only the named slots change. The cache may not overlap K, V or slots (GPTQ_ERR_ARG).
+ * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
 gptq_status kv_cache_write(const void* K, const void* V, int dtype, int64_t n_tokens,
                            int64_t k_stride, int64_t v_stride, int n_heads, int head_dim,
                            const int64_t* slots, int64_t n_slots, int bits, int group_size,
@@ -473,7 +476,7 @@ gptq_status kv_cache_write(const void* K, const void* V, int dtype, int64_t n_to
  *   K, V     device [total x n_heads x head_dim], fp16, fp32 or bf16 (dtype), 16-byte aligned.
  *   status_dev device int or NULL: set to GPTQ_ERR_ARG if a position is behind max_pages pages or
  *            a page is outside 0 .. n_pages - 1 (such rows are written as zeros).
- * Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
+ * K and V may overlap neither each other nor the cache (GPTQ_ERR_ARG). Asynchronous. Errors: ARG, CUDA, UNSUPPORTED. */
 gptq_status kv_cache_read(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros,
                           int64_t n_pages, int page_size, int n_heads, int head_dim, int bits,
                           int group_size, const int32_t* page_table, int n_seqs, int max_pages,

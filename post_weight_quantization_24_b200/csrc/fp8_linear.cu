@@ -852,6 +852,16 @@ extern "C" gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int6
     if (!X8 || !x_scales || !W8 || !w_scales || !Y || !al(X8, 16) || !al(W8, 16) || !al(Y, 16) ||
         (R && !al(R, 16)) || !al(x_scales, 4) || !al(w_scales, 4) || !al(status_dev, 4))
         return GPTQ_ERR_ARG;
+    // Y is written while other tiles are still read: R may be Y itself (every value is read by
+    // whoever writes it), and nothing else may share memory with Y
+    const int64_t n_kb = (d_in + 127) / 128;
+    const int64_t y_bytes = gq::range_bytes(n_tokens * d_out, y_dtype == GPTQ_DTYPE_F32 ? 4 : 2);
+    if ((R != Y && gq::overlap(Y, y_bytes, R, y_bytes)) ||
+        gq::overlap(Y, y_bytes, X8, n_tokens * d_in) ||
+        gq::overlap(Y, y_bytes, W8, static_cast<int64_t>(d_out) * d_in) ||
+        gq::overlap(Y, y_bytes, x_scales, 4 * n_kb * n_tokens) ||
+        gq::overlap(Y, y_bytes, w_scales, 4 * n_kb * ((static_cast<int64_t>(d_out) + 127) / 128)))
+        return GPTQ_ERR_ARG;
     GPTQ_TRY(gq::check_device());
     gq::F8Params p{};
     p.n_tok = static_cast<int>(n_tokens);

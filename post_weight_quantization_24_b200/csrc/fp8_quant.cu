@@ -266,6 +266,14 @@ static bool fp8_dtype_ok(int t) {
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 static bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
+// Other CTAs read the input while one writes its codes and scales, so these may not share memory.
+static bool fp8_apart(const void* x, int dtype, int64_t values, const void* codes,
+                      const void* scales, int64_t n_scales) {
+    const int64_t x_bytes = range_bytes(values, dtype == GPTQ_DTYPE_F32 ? 4 : 2);
+    return !overlap(x, x_bytes, codes, values) && !overlap(x, x_bytes, scales, 4 * n_scales) &&
+           !overlap(codes, values, scales, 4 * n_scales);
+}
+
 }  // namespace gq
 
 extern "C" {
@@ -277,6 +285,8 @@ gptq_status fp8_quantize_act(const void* X, int x_dtype, int64_t n_tokens, int d
     if (d < 16 || d % 16 || d > 65536) return GPTQ_ERR_ARG;
     if (n_tokens == 0) return GPTQ_OK;
     if (!X || !codes || !scales || !gq::al16(X) || !gq::al16(codes) || !gq::al4(scales))
+        return GPTQ_ERR_ARG;
+    if (!gq::fp8_apart(X, x_dtype, n_tokens * d, codes, scales, n_tokens * ((d + 127) / 128)))
         return GPTQ_ERR_ARG;
     GPTQ_TRY(gq::check_device());
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -292,6 +302,9 @@ gptq_status fp8_quantize_weight(const void* W, int w_dtype, int d_out, int d_in,
     if (!W || !codes || !scales || !gq::fp8_dtype_ok(w_dtype)) return GPTQ_ERR_ARG;
     if (d_out < 1 || d_in < 16 || d_in % 16 || d_in > 65536) return GPTQ_ERR_ARG;
     if (!gq::al16(W) || !gq::al16(codes) || !gq::al4(scales)) return GPTQ_ERR_ARG;
+    if (!gq::fp8_apart(W, w_dtype, static_cast<int64_t>(d_out) * d_in, codes, scales,
+                       ((static_cast<int64_t>(d_out) + 127) / 128) * ((d_in + 127) / 128)))
+        return GPTQ_ERR_ARG;
     GPTQ_TRY(gq::check_device());
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (w_dtype) {

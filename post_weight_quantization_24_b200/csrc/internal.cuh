@@ -7,6 +7,17 @@
 
 namespace gq {
 
+// Bytes of a range of values; no memory is as large as the bound that keeps the product in 64 bits.
+inline int64_t range_bytes(int64_t values, int size) {
+    return (values < (int64_t(1) << 56) ? values : int64_t(1) << 56) * size;
+}
+// Whether two ranges of device memory share a byte (a null or empty one shares none).
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uintptr_t>(b_bytes) &&
+           y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 // The library's second stream on the current device and the events that order it with the
 // caller's stream (created on first use; one set per device). Hold side_streams_mutex() while
 // enqueuing work that uses them.

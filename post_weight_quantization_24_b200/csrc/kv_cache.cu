@@ -585,6 +585,13 @@ static gptq_status kv_params(int dtype, int n_heads, int head_dim, int bits, int
     return GPTQ_OK;
 }
 
+// Whether [x, x + bytes) shares memory with one of the cache's arrays.
+static bool kv_in_cache(const KvParams& p, int bits, const void* x, int64_t bytes) {
+    const int64_t rows = 2 * p.n_slots;
+    return overlap(x, bytes, p.codes, rows * p.width * bits / 8) ||
+           overlap(x, bytes, p.scales, rows * p.ng * 2) || overlap(x, bytes, p.zeros, rows * p.ng * 2);
+}
+
 }  // namespace gq
 
 extern "C" {
@@ -605,6 +612,13 @@ gptq_status kv_cache_write(const void* K, const void* V, int dtype, int64_t n_to
     if (n_tokens == 0) return GPTQ_OK;
     if (!K || !V || !slots || !gq::kv_aligned(K, 16) || !gq::kv_aligned(V, 16) ||
         !gq::kv_aligned(slots, 8))
+        return GPTQ_ERR_ARG;
+    // tokens are read while others' codes are written
+    auto bytes = [&](int64_t stride) {
+        return gq::range_bytes((n_tokens - 1) * stride + p.width, dtype == GPTQ_DTYPE_F32 ? 4 : 2);
+    };
+    if (gq::kv_in_cache(p, bits, K, bytes(k_stride)) || gq::kv_in_cache(p, bits, V, bytes(v_stride)) ||
+        gq::kv_in_cache(p, bits, slots, 8 * n_tokens))
         return GPTQ_ERR_ARG;
     GPTQ_TRY(gq::check_device());
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -634,6 +648,10 @@ gptq_status kv_cache_read(const uint8_t* codes, const uint16_t* scales, const ui
     if (total == 0 || n_seqs == 0) return GPTQ_OK;
     if ((!page_table && max_pages) || !cu_lens || !K || !V || !gq::kv_aligned(page_table, 4) ||
         !gq::kv_aligned(cu_lens, 4) || !gq::kv_aligned(K, 16) || !gq::kv_aligned(V, 16))
+        return GPTQ_ERR_ARG;
+    const int64_t out = gq::range_bytes(total * p.width, dtype == GPTQ_DTYPE_F32 ? 4 : 2);
+    if (gq::overlap(K, out, V, out) || gq::kv_in_cache(p, bits, K, out) ||
+        gq::kv_in_cache(p, bits, V, out))
         return GPTQ_ERR_ARG;
     GPTQ_TRY(gq::check_device());
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
