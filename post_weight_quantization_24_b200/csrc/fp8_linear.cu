@@ -63,11 +63,22 @@ __device__ __forceinline__ void f8_promote(uint64_t* acc, const uint32_t (&r)[NC
     for (int k = 0; k < NC / 2; ++k) fma_f32x2(acc[k], f32x2(r[2 * k], r[2 * k + 1]), f);
 }
 
-// Wait of a whole warp, every lane on the barrier itself: true if it completed, else the timeout
-// is recorded.
+// Wait of a whole warp, every lane on the barrier itself: true if it completed for all of them, else
+// the timeout is recorded. The lanes leave together with one answer, because what follows needs them
+// all. With WATCH the wait also ends once another wait of the CTA has given up, which a caller that
+// carries on after a give-up needs; to test the flag ahead of the wait instead would let each lane
+// decide by itself, and could send some past a vote that the others are in.
+template <bool WATCH = false>
 __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, int* status,
                                              volatile int* abort_flag) {
-    if (__all_sync(0xffffffffu, mbar_wait(bar, parity))) return true;
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = mbar_try_wait(bar, parity)) && clock64() - t0 <= kWaitLimitCycles) {
+            if (WATCH && *abort_flag) break;
+        }
+    }
+    if (__all_sync(0xffffffffu, ok)) return true;
     set_status(status, GPTQ_ERR_TIMEOUT);
     *abort_flag = 1;
     return false;
@@ -262,9 +273,9 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
                 for (int u = 0; u < 4; ++u) factors[e + u * C::EPI_THREADS] = fx[u] * fw[u];
                 asm volatile("bar.sync 1, %0;" ::"n"(C::EPI_THREADS) : "memory");
             }
-            // a wait that gave up sets the flag and lets the loop run out: the barriers above
-            // need every promotion thread
-            if (!*abort_flag) f8_warp_wait(&acc_full[b], (it / C::ACCS) & 1, p.status, abort_flag);
+            // after a wait that gave up the loop runs out: the barriers above need every
+            // promotion thread
+            f8_warp_wait<true>(&acc_full[b], (it / C::ACCS) & 1, p.status, abort_flag);
             tc_fence_after();
             const uint32_t t_addr = t_addr0 + static_cast<uint32_t>(b * NT);
             const float* f = factors + (it % C::FBLK) * NT + g * C::EC;
