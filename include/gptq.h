@@ -510,6 +510,13 @@ unsigned long long gptq_launch_count(void);
  * ------------------------------------------------------------------------------------------ */
 gptq_status gptq_test_stall_factor(int on);
 
+/* The same for fp8_linear. With rank >= 0, in every cluster of CTAs the producer of CTA `rank`
+ * gives up after a few blocks of its work, if its part of the layer has so many, and waits are
+ * limited to about 1 ms: such a call writes GPTQ_ERR_TIMEOUT to its status_dev and leaves Y
+ * unspecified; the context stays usable. rank < 0 restores normal operation. Process-wide, read
+ * when a call is enqueued, for tests only. Errors: CUDA, UNSUPPORTED. */
+gptq_status gptq_test_stall_fp8(int rank);
+
 #ifdef __cplusplus
 }
 #endif

@@ -531,6 +531,11 @@ gptq_status gptq_test_stall_factor(int on) {
     return factor_stall_set(on);
 }
 
+gptq_status gptq_test_stall_fp8(int rank) {
+    GPTQ_TRY(check_device());
+    return fp8_stall_set(rank);
+}
+
 int gptq_profile_read(float* ms_out, int max_stages) {
     std::lock_guard<std::mutex> lock(g_prof.mu);
     const int n = max_stages < kStages ? max_stages : kStages;

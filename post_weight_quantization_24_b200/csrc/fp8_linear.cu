@@ -36,7 +36,21 @@ struct F8Params {
     void* Y;
     int vec_ok;           // rows of Y and R start on 16-byte boundaries
     int* status;
+    long long wait_limit; // cycles after which a wait gives up
+    int stall_rank;       // test switch: the CTA of a cluster whose producer gives up, or -1
 };
+
+// Test switch for the give-up paths (set by gptq_test_stall_fp8, read when a call is enqueued): the
+// producer of one CTA in each cluster behaves as if its wait for a stage had run out, a few
+// blocks into its work. Copies, MMAs and sums are in flight then, in its CTA and in the others,
+// whose own waits give up after STALL_LIMIT_CYCLES.
+static std::atomic<int> g_fp8_stall{-1};
+constexpr long long STALL_LIMIT_CYCLES = 2000000;   // about 1 ms
+
+gptq_status fp8_stall_set(int rank) {
+    g_fp8_stall.store(rank < 0 ? -1 : rank);
+    return GPTQ_OK;
+}
 
 // NC accumulated columns of one row -> Y (+ R), value by value: for rows that do not all start on
 // 16-byte boundaries.
@@ -69,17 +83,17 @@ __device__ __forceinline__ void f8_promote(uint64_t* acc, const uint32_t (&r)[NC
 // carries on after a give-up needs; to test the flag ahead of the wait instead would let each lane
 // decide by itself, and could send some past a vote that the others are in.
 template <bool WATCH = false>
-__device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, int* status,
+__device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, const F8Params& p,
                                              volatile int* abort_flag) {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
         const long long t0 = clock64();
-        while (!(ok = mbar_try_wait(bar, parity)) && clock64() - t0 <= kWaitLimitCycles) {
+        while (!(ok = mbar_try_wait(bar, parity)) && clock64() - t0 <= p.wait_limit) {
             if (WATCH && *abort_flag) break;
         }
     }
     if (__all_sync(0xffffffffu, ok)) return true;
-    set_status(status, GPTQ_ERR_TIMEOUT);
+    set_status(p.status, GPTQ_ERR_TIMEOUT);
     *abort_flag = 1;
     return false;
 }
@@ -159,6 +173,9 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
         tma_load_2d(sa, &wmap, &full[st], x, c0);
         tma_load_2d(sa + C::A_BYTES, &xmap, &full[st], x, t0);
     };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return mbar_wait_cycles(bar, parity, p.wait_limit);
+    };
     const int first = min(C::STAGES, n_kb);
     // The promotion threads' scales of blocks it0 .. it0 + FBLK - 1, four values each, all asked for at
     // once (entries past the last block or token repeat the last: they are not used).
@@ -207,7 +224,8 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
         if (lane == 0) {
             int it = first;
             for (; it < n_kb && !*abort_flag; ++it) {
-                if (!mbar_wait(&empty[it % C::STAGES], ((it / C::STAGES) & 1) ^ 1)) {
+                if ((it == C::STAGES + 1 && rank == p.stall_rank) ||
+                    !wait(&empty[it % C::STAGES], ((it / C::STAGES) & 1) ^ 1)) {
                     set_status(p.status, GPTQ_ERR_TIMEOUT);
                     *abort_flag = 1;
                     break;
@@ -216,7 +234,7 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
             }
             const int n_tail = it < C::STAGES ? it : C::STAGES;
             for (int k = it - n_tail; k < it; ++k) {
-                if (!mbar_wait(&full[k % C::STAGES], (k / C::STAGES) & 1)) {
+                if (!wait(&full[k % C::STAGES], (k / C::STAGES) & 1)) {
                     set_status(p.status, GPTQ_ERR_TIMEOUT);
                     *abort_flag = 1;
                 }
@@ -228,8 +246,8 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
             bool ok = true;
             for (int it = warp - 1; it < n_kb && !*abort_flag; it += 2) {
                 const int st = it % C::STAGES, b = it % C::ACCS;
-                if (!mbar_wait(&acc_empty[b], ((it / C::ACCS) & 1) ^ 1) ||
-                    !mbar_wait(&full[st], (it / C::STAGES) & 1)) {
+                if (!wait(&acc_empty[b], ((it / C::ACCS) & 1) ^ 1) ||
+                    !wait(&full[st], (it / C::STAGES) & 1)) {
                     ok = false;
                     break;
                 }
@@ -251,7 +269,7 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
                 *abort_flag = 1;
             }
             umma_commit(&drained[warp - 1]);
-            if (!mbar_wait(&drained[warp - 1], 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
+            if (!wait(&drained[warp - 1], 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
         }
         __syncwarp();
     } else {
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
             }
             // after a wait that gave up the loop runs out: the barriers above need every
             // promotion thread
-            f8_warp_wait<true>(&acc_full[b], (it / C::ACCS) & 1, p.status, abort_flag);
+            f8_warp_wait<true>(&acc_full[b], (it / C::ACCS) & 1, p, abort_flag);
             tc_fence_after();
             const uint32_t t_addr = t_addr0 + static_cast<uint32_t>(b * NT);
             const float* f = factors + (it % C::FBLK) * NT + g * C::EC;
@@ -314,7 +332,7 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
                          mapa_shared(smem_u32(recv_full), static_cast<uint32_t>(owner)));
         }
         // this CTA's share of the tokens: a warp takes a token, a lane four channels
-        const bool got = f8_warp_wait(recv_full, 0, p.status, abort_flag);
+        const bool got = f8_warp_wait(recv_full, 0, p, abort_flag);
         const int col = c0 + 4 * lane;
         for (int i = warp - 3; i < share; i += C::EPI_WARPS) {
             const int row = t0 + rank * share + i;
@@ -363,11 +381,13 @@ __global__ void __launch_bounds__(f8s::Cfg<NT>::THREADS, f8s::Cfg<NT>::PER_SM)
         tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
     if (*abort_flag) {
-        // sums for this CTA may still be under way: it stays until the others have left (they need
-        // nothing of it) or wait here too
+        // Sums for this CTA may still be under way: every CTA sends its own, whatever else it gave
+        // up. This CTA stays until the others have sent theirs (they have left, needing nothing of
+        // it, or wait here too) and until all have arrived.
         __syncwarp();
         cluster_arrive();
         cluster_wait();
+        if (threadIdx.x == 0) wait(recv_full, 0);
     }
 }
 
@@ -427,7 +447,7 @@ template <typename T>
 __device__ __forceinline__ bool f8_store_boxes(const CUtensorMap* ymap, const CUtensorMap* rmap,
                                                bool res, int n_tok, int d_out, int row0, int col0,
                                                const uint64_t (&acc)[f8p::HN / 2], uint8_t* buf,
-                                               uint64_t* bar, uint32_t& r_phase, int* status,
+                                               uint64_t* bar, uint32_t& r_phase, const F8Params& p,
                                                volatile int* abort_flag) {
     constexpr int N = Vec<T>::N, COLS = 8 * N, ROUND = 2 * COLS;
     const int lane = lane_id();
@@ -441,7 +461,7 @@ __device__ __forceinline__ bool f8_store_boxes(const CUtensorMap* ymap, const CU
             __syncwarp();
         }
         if (res) {
-            if (!f8_warp_wait(bar, r_phase, status, abort_flag)) return false;
+            if (!f8_warp_wait(bar, r_phase, p, abort_flag)) return false;
             r_phase ^= 1;
         }
 #pragma unroll
@@ -641,7 +661,7 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
                     sx_next = __ldg(sx);
                     sw_next = __ldg(sw + kb + 1);
                 }
-                if (!f8_warp_wait(&acc_full[b], (it >> 1) & 1, p.status, abort_flag)) {
+                if (!f8_warp_wait(&acc_full[b], (it >> 1) & 1, p, abort_flag)) {
                     stop = true;
                     break;
                 }
@@ -676,7 +696,7 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
                     __syncwarp();
                 }
                 stop = !f8_store_boxes<T>(&ymap, &rmap, res, p.n_tok, p.d_out, m0 + row_in, col0, acc,
-                                          buf, r_bar, r_phase, p.status, abort_flag);
+                                          buf, r_bar, r_phase, p, abort_flag);
             } else {
                 f8_store<T, f8p::HN>(p, m0 + row_in + lane, col0, acc);
             }
@@ -884,6 +904,8 @@ extern "C" gptq_status fp8_linear(const uint8_t* X8, const float* x_scales, int6
     p.R = R;
     p.Y = Y;
     p.status = status_dev;
+    p.stall_rank = gq::g_fp8_stall.load();
+    p.wait_limit = p.stall_rank < 0 ? gq::kWaitLimitCycles : gq::STALL_LIMIT_CYCLES;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (y_dtype) {
         case GPTQ_DTYPE_F16: return gq::fp8_linear_launch<__half>(X8, W8, p, s);

@@ -85,6 +85,10 @@ gptq_status factor_inverse_launch(float* A, int d, float* Dinv, float* X, float*
 // Test switch: the diagonal-block kernel waits on a barrier nothing arrives at (bounded).
 gptq_status factor_stall_set(int on);
 
+// fp8_linear.cu
+// Test switch: the producer of a cluster's CTA `rank` gives up in every call (bounded); < 0: off.
+gptq_status fp8_stall_set(int rank);
+
 // gptq.cu
 // Per-row images of U's diagonal blocks for the column loop: img [d x 128],
 // img[R][k] = U[R][R+1+k] inside R's block of block_size columns (else 0); rdiag[R] = 1/U[R][R].

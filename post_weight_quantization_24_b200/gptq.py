@@ -97,6 +97,7 @@ _SIGNATURES = {
     "gptq_profile_read": ([ctypes.POINTER(_F), _I], _I),
     "gptq_launch_count": ([], ctypes.c_ulonglong),
     "gptq_test_stall_factor": ([_I], _I),
+    "gptq_test_stall_fp8": ([_I], _I),
 }
 
 
@@ -717,6 +718,12 @@ def launch_count() -> int:
 def test_stall_factor(on: bool) -> None:
     """Test hook: make the factorisation's bounded wait run out (see include/gptq.h)."""
     _check(lib().gptq_test_stall_factor(int(bool(on))), "gptq_test_stall_factor")
+
+
+def test_stall_fp8(rank: int | None) -> None:
+    """Test hook: in fp8_linear the producer of each cluster's CTA ``rank`` gives up (None: off; see
+    include/gptq.h)."""
+    _check(lib().gptq_test_stall_fp8(-1 if rank is None else int(rank)), "gptq_test_stall_fp8")
 
 
 def status_string(status: int) -> str:
