@@ -280,6 +280,10 @@ __device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t v, 
         "r"(v), "r"(cluster_bar)
         : "memory");
 }
+// store a 32-bit value into the shared memory of a CTA of the cluster (read after a cluster barrier)
+__device__ __forceinline__ void st_shared_cluster_b32(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
 // arrive on an mbarrier given by its shared::cluster address (possibly another CTA's)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)

@@ -501,6 +501,18 @@ __device__ __forceinline__ void f8_tile(const F8Params& p, int t, int& m0, int& 
     n0 = (rem / band_m) * f8p::PT;
 }
 
+// Block kb of a tile into stage st: this CTA's tokens and its half of the channels. Both CTAs' bytes
+// complete on the leader's barrier, which the leader arms for both.
+__device__ __forceinline__ void f8_pair_load(const CUtensorMap* xmap, const CUtensorMap* wmap,
+                                             uint8_t* smem, uint64_t* full, bool leader, int st, int kb,
+                                             int m0, int n0) {
+    uint8_t* sa = smem + st * f8p::STAGE;
+    if (leader) mbar_arrive_expect_tx(&full[st], 2 * f8p::STAGE);
+    const uint32_t fb = mapa_shared(smem_u32(&full[st]), 0);
+    tma_load_2d_pair(sa, xmap, fb, kb * f8p::BK, m0);
+    tma_load_2d_pair(sa + f8p::A_BYTES, wmap, fb, kb * f8p::BK, n0);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(f8p::THREADS, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
@@ -517,11 +529,25 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
     uint64_t* drained = acc_empty + 2;               // [2] leader, one per issuer
     uint64_t* r_full = drained + 2;                  // [EPI_WARPS] each CTA: a warp's part of R
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(r_full + f8p::EPI_WARPS);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    // whether this CTA and the other one have given up, and then the blocks that each has loaded
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
+    volatile uint32_t* loaded = tmem_slot + 4;                                   // [2], by rank
 
     const int warp = warp_id(), lane = lane_id();
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return mbar_wait_cycles(bar, parity, p.wait_limit);
+    };
+    auto tell_other = [&](volatile void* at, uint32_t v) {
+        st_shared_cluster_b32(mapa_shared(smem_u32(const_cast<const void*>(at)), rank ^ 1), v);
+    };
+    // this CTA's first token and first channel to load of tile t
+    auto tile_of = [&](int t, int& m0, int& n0) {
+        f8_tile(p, t, m0, n0);
+        m0 += f8p::BM * static_cast<int>(rank);
+        n0 += f8p::BNC * static_cast<int>(rank);
+    };
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < f8p::STAGES; ++s) {
@@ -534,7 +560,7 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
             mbar_init(&drained[b], 1);
         }
         for (int w = 0; w < f8p::EPI_WARPS; ++w) mbar_init(&r_full[w], 1);
-        *abort_flag = 0;
+        abort_flag[0] = abort_flag[1] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&xmap);
         tma_prefetch_desc(&wmap);
@@ -557,34 +583,30 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
             int it = 0;
             for (int t = cluster; t < p.n_tiles && !*abort_flag; t += n_clusters) {
                 int m0, n0;
-                f8_tile(p, t, m0, n0);
-                m0 += f8p::BM * static_cast<int>(rank);
-                n0 += f8p::BNC * static_cast<int>(rank);
+                tile_of(t, m0, n0);
                 for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
                     const int st = it % f8p::STAGES;
-                    if (!mbar_wait(&empty[st], ((it / f8p::STAGES) & 1) ^ 1)) {
+                    if ((it == f8p::STAGES + 1 && static_cast<int>(rank) == p.stall_rank) ||
+                        !wait(&empty[st], ((it / f8p::STAGES) & 1) ^ 1)) {
                         set_status(p.status, GPTQ_ERR_TIMEOUT);
                         *abort_flag = 1;
                         break;
                     }
-                    uint8_t* sa = smem + st * f8p::STAGE;
-                    if (leader) mbar_arrive_expect_tx(&full[st], 2 * f8p::STAGE);
-                    const uint32_t fb = mapa_shared(smem_u32(&full[st]), 0);
-                    tma_load_2d_pair(sa, &xmap, fb, kb * f8p::BK, m0);
-                    tma_load_2d_pair(sa + f8p::A_BYTES, &wmap, fb, kb * f8p::BK, n0);
+                    f8_pair_load(&xmap, &wmap, smem, full, leader, st, kb, m0, n0);
                 }
             }
-            // the leader's stage barriers count both CTAs' bytes: once it has seen the last
-            // stages complete, no copy of either CTA is still writing shared memory
-            if (leader) {
-                const int n_tail = it < f8p::STAGES ? it : f8p::STAGES;
-                for (int k = it - n_tail; k < it; ++k) {
-                    if (!mbar_wait(&full[k % f8p::STAGES], (k / f8p::STAGES) & 1)) {
-                        set_status(p.status, GPTQ_ERR_TIMEOUT);
-                        *abort_flag = 1;
-                    }
+            // The last stages' releases: every block that was loaded has then been multiplied, so no
+            // copy is in flight, and no release is still on its way to this CTA's barriers. After a
+            // give-up the copies are seen to below.
+            const int n_tail = it < f8p::STAGES ? it : f8p::STAGES;
+            for (int k = it - n_tail; k < it && !*abort_flag; ++k) {
+                if (!wait(&empty[k % f8p::STAGES], (k / f8p::STAGES) & 1)) {
+                    set_status(p.status, GPTQ_ERR_TIMEOUT);
+                    *abort_flag = 1;
                 }
             }
+            loaded[rank] = static_cast<uint32_t>(it);
+            if (*abort_flag) tell_other(abort_flag + 1, 1);
         } else if ((warp == 1 || warp == 2) && leader && lane == 0) {
             // ---------------- MMA issuers (leader), every other block each ----------------
             const int b = warp - 1;
@@ -595,7 +617,7 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
             int st = b;
             uint32_t st_phase = 0, acc_phase = 1;
             for (long long it = b; it < blocks && !*abort_flag; it += 2) {
-                if (!mbar_wait(&full[st], st_phase) || !mbar_wait(&acc_empty[b], acc_phase)) {
+                if (!wait(&full[st], st_phase) || !wait(&acc_empty[b], acc_phase)) {
                     ok = false;
                     break;
                 }
@@ -622,7 +644,11 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
             }
             // every MMA must have finished before either CTA releases TMEM or leaves
             umma_commit_pair_mc(&drained[b], 0x1);
-            if (!mbar_wait(&drained[b], 0)) set_status(p.status, GPTQ_ERR_TIMEOUT);
+            if (!wait(&drained[b], 0)) {
+                set_status(p.status, GPTQ_ERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (*abort_flag) tell_other(abort_flag + 1, 1);
         }
         __syncwarp();
     } else {
@@ -702,7 +728,8 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
             }
         }
         // a residual that was asked for and not used (after a timeout) must have landed
-        if (boxes && res && stop && lane == 0) mbar_wait(r_bar, r_phase);
+        if (boxes && res && stop && lane == 0) wait(r_bar, r_phase);
+        if (stop && lane == 0) tell_other(abort_flag + 1, 1);
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
@@ -711,6 +738,29 @@ __global__ void __launch_bounds__(f8p::THREADS, 1)
     __syncthreads();
     cluster_sync();     // neither CTA leaves while the pair's MMAs, copies or arrivals may touch it
     tc_fence_after();
+    if (const int2 gave_up = *reinterpret_cast<const int2*>(const_cast<const int*>(abort_flag));
+        gave_up.x || gave_up.y) {
+        // One of the two gave up, and its producer may have stopped before the other's. The one that
+        // is behind (by STAGES blocks at most: a stage is released to both) loads what the other has
+        // loaded, so that the leader's barriers complete for both CTAs' copies. No MMA is left to
+        // read the stages.
+        if (threadIdx.x == 0) tell_other(&loaded[rank], loaded[rank]);
+        __syncwarp();
+        cluster_sync();
+        if (threadIdx.x == 0) {
+            const int blocks = static_cast<int>(max(loaded[0], loaded[1]));
+            for (int it = static_cast<int>(loaded[rank]); it < blocks; ++it) {
+                int m0, n0;
+                tile_of(cluster + it / p.n_kb * n_clusters, m0, n0);
+                f8_pair_load(&xmap, &wmap, smem, full, leader, it % f8p::STAGES, it % p.n_kb, m0, n0);
+            }
+            if (leader)
+                for (int it = max(0, blocks - f8p::STAGES); it < blocks; ++it)
+                    wait(&full[it % f8p::STAGES], (it / f8p::STAGES) & 1);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 1) tmem_dealloc_pair(tmem_base, f8p::TMEM_COLS);
 }
 
