@@ -415,6 +415,10 @@ gptq_status fp8_quantize_weight(const void* W, int w_dtype, int d_out, int d_in,
  *           (sum over the block's channels of X8[t][c] * W8[o][c])  + R[t][o],
  * the block's inner sum on the tensor cores from zero, the sum over blocks in fp32 with
  * round-to-nearest, one rounding to Y's type.
+ * A block's two scales are multiplied in fp32 before they meet its sum (which is 0 or 2^-18 to 2^25
+ * large). Where that product is below 2^-126 it has lost bits, which puts a term off by up to
+ * 2^-125, no more than fp32's smallest normal numbers; where it passes fp32's range (activations times
+ * weights of 2^145 and more) the term is infinite, or NaN for a sum of 0.
  *   X8, x_scales   as fp8_quantize_act writes them; 0 <= n_tokens < 2^31 (0 is a no-op).
  *   W8, w_scales   as fp8_quantize_weight writes them.   d_in: a multiple of 16, <= 65536.
  *                  d_out >= 1.
@@ -467,7 +471,9 @@ gptq_status kv_cache_write(const void* K, const void* V, int dtype, int64_t n_to
 
 /* Read the context of n_seqs sequences back, packed one after the other:
  * K[t], V[t] = out_type(scale * (code - zero)) (one rounding) of position t - cu_lens[b] of the
- * sequence b with cu_lens[b] <= t < cu_lens[b+1].
+ * sequence b with cu_lens[b] <= t < cu_lens[b+1]. The scale is rounded up, so a group's largest value
+ * can read back as much as half a step above what was written; in fp16 that is infinite from 65520 on
+ * (a one-sided group that ends at 65504 reads back 255 * 257 = 65535). Read such caches as bf16 or fp32.
  *   page_table device int32 [n_seqs x max_pages]: the page of a sequence's positions
  *            j*page_size .. is entry j. Entries behind a sequence's last page are not read.
  *   cu_lens  device int32 [n_seqs + 1], ascending: running sums of the lengths (0 allowed).

@@ -574,7 +574,9 @@ def fp8_linear(X8: torch.Tensor, x_scales: torch.Tensor, W8: torch.Tensor,
                out: torch.Tensor | None = None, dtype: torch.dtype = torch.float16,
                status: torch.Tensor | None = None) -> torch.Tensor:
     """Y = X̂·Ŵᵀ + R [n, d_out] (fp16/fp32/bf16) from fp8_quantize_act's and
-    fp8_quantize_weight's codes and scales; R has Y's type and may be ``out``."""
+    fp8_quantize_weight's codes and scales; R has Y's type and may be ``out``. Products of two
+    scales are fp32 numbers (include/gptq.h says what that bounds). ``status`` (int32, zeroed by the
+    caller): GPTQ_ERR_TIMEOUT if a device-side wait gave up; Y is unspecified then."""
     dev = _device()
     _require(X8, "X8", _E4M3, None, dev)
     _require(W8, "W8", _E4M3, None, dev)
@@ -672,7 +674,9 @@ def kv_cache_read(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
     """The context of every sequence, packed: (K, V) [total, n_heads, head_dim] of positions
     0 .. len-1 of each sequence in turn. page_table int32 [n_seqs, max_pages], cu_lens int32
     [n_seqs + 1] (running sums of the lengths). Rows behind cu_lens[-1] are left as they were;
-    positions without a page of the cache come as zeros and set ``status`` to GPTQ_ERR_ARG."""
+    positions without a page of the cache come as zeros and set ``status`` to GPTQ_ERR_ARG. In
+    float16, values that come to 65520 or more are infinite (keys near 65504, whose scale was
+    rounded up)."""
     dev = _device()
     n_pages, page_size, H, D, g = _cache_dims(codes, scales, zeros, bits, dev)
     _require(page_table, "page_table", torch.int32, None, dev)
