@@ -523,6 +523,12 @@ gptq_status gptq_test_stall_factor(int on);
  * when a call is enqueued, for tests only. Errors: CUDA, UNSUPPORTED. */
 gptq_status gptq_test_stall_fp8(int rank);
 
+/* With on != 0, fp8_linear serves its large calls as it does where its kernel for pairs of CTAs
+ * cannot be launched (a build whose compiler gave that kernel other registers than its warps share
+ * out): on the streaming kernel. on = 0 restores normal operation. Process-wide, for tests only.
+ * Errors: CUDA, UNSUPPORTED. */
+gptq_status gptq_test_fp8_no_pair(int on);
+
 #ifdef __cplusplus
 }
 #endif

@@ -536,6 +536,11 @@ gptq_status gptq_test_stall_fp8(int rank) {
     return fp8_stall_set(rank);
 }
 
+gptq_status gptq_test_fp8_no_pair(int on) {
+    GPTQ_TRY(check_device());
+    return fp8_no_pair_set(on);
+}
+
 int gptq_profile_read(float* ms_out, int max_stages) {
     std::lock_guard<std::mutex> lock(g_prof.mu);
     const int n = max_stages < kStages ? max_stages : kStages;

@@ -52,6 +52,14 @@ gptq_status fp8_stall_set(int rank) {
     return GPTQ_OK;
 }
 
+// Test switch: calls behave as on a build whose pair kernel cannot be launched.
+static std::atomic<int> g_fp8_no_pair{0};
+
+gptq_status fp8_no_pair_set(int on) {
+    g_fp8_no_pair.store(on ? 1 : 0);
+    return GPTQ_OK;
+}
+
 // NC accumulated columns of one row -> Y (+ R), value by value: for rows that do not all start on
 // 16-byte boundaries.
 template <typename T, int NC>
@@ -854,18 +862,30 @@ struct F8MapType<float> {
     static constexpr CUtensorMapDataType value = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 };
 
+// Whether this device can run the pair kernel: the warpgroups' register shares add up to what a
+// launch with REGS per thread has, which is the compiler's to give. Without it the streaming kernel
+// serves every call.
+template <typename T>
+static gptq_status fp8_pair_usable(bool* usable) {
+    static std::atomic<unsigned long long> done{0}, too_few{0};
+    int dev = 0;
+    GPTQ_CUDA_TRY(cudaGetDevice(&dev));
+    const unsigned long long bit = 1ull << (dev & 63);
+    GPTQ_TRY(f8_once(done, [&]() -> gptq_status {
+        GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_pair_kernel<T>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, f8p::SMEM));
+        cudaFuncAttributes fa;
+        GPTQ_CUDA_TRY(cudaFuncGetAttributes(&fa, fp8_pair_kernel<T>));
+        if (fa.numRegs < f8p::REGS) too_few.fetch_or(bit);
+        return GPTQ_OK;
+    }));
+    *usable = !(too_few.load() & bit) && !g_fp8_no_pair.load();
+    return GPTQ_OK;
+}
+
 template <typename T>
 static gptq_status fp8_pair_launch(const uint8_t* X8, const uint8_t* W8, F8Params& p,
                                    cudaStream_t s) {
-    static std::atomic<unsigned long long> done{0};
-    GPTQ_TRY(f8_once(done, []() -> gptq_status {
-        GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp8_pair_kernel<T>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, f8p::SMEM));
-        // the warpgroups' register shares add up to what a launch with REGS per thread has
-        cudaFuncAttributes fa;
-        GPTQ_CUDA_TRY(cudaFuncGetAttributes(&fa, fp8_pair_kernel<T>));
-        return fa.numRegs < f8p::REGS ? GPTQ_ERR_UNSUPPORTED : GPTQ_OK;
-    }));
     CUtensorMap xmap, wmap;
     GPTQ_TRY(encode_tensor_map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(X8),
                                   p.d_in, p.n_tok, p.d_in, f8p::BK, f8p::BM,
@@ -909,8 +929,11 @@ static gptq_status fp8_linear_launch(const uint8_t* X8, const uint8_t* W8, F8Par
         const long long tiles = static_cast<long long>((p.n_tok - 1) / 128 + 1) * ((p.d_out - 1) / 128 + 1);
         const int splits = f8_splits(tiles, p.n_kb, 1);
         const long long waves = (tiles * splits + num_sms() - 1) / num_sms();
-        if (5 * pair_waves * p.n_kb <= 6 * waves * ((p.n_kb + splits - 1) / splits))
-            return fp8_pair_launch<T>(X8, W8, p, s);
+        if (5 * pair_waves * p.n_kb <= 6 * waves * ((p.n_kb + splits - 1) / splits)) {
+            bool usable = false;
+            GPTQ_TRY(fp8_pair_usable<T>(&usable));
+            if (usable) return fp8_pair_launch<T>(X8, W8, p, s);
+        }
     }
     if (p.n_tok <= 16) return fp8_stream_launch<T, 16>(X8, W8, p, s);
     if (p.n_tok <= 32) return fp8_stream_launch<T, 32>(X8, W8, p, s);

@@ -88,6 +88,8 @@ gptq_status factor_stall_set(int on);
 // fp8_linear.cu
 // Test switch: the producer of a cluster's CTA `rank` gives up in every call (bounded); < 0: off.
 gptq_status fp8_stall_set(int rank);
+// Test switch: the streaming kernel serves every call.
+gptq_status fp8_no_pair_set(int on);
 
 // gptq.cu
 // Per-row images of U's diagonal blocks for the column loop: img [d x 128],

@@ -98,6 +98,7 @@ _SIGNATURES = {
     "gptq_launch_count": ([], ctypes.c_ulonglong),
     "gptq_test_stall_factor": ([_I], _I),
     "gptq_test_stall_fp8": ([_I], _I),
+    "gptq_test_fp8_no_pair": ([_I], _I),
 }
 
 
@@ -728,6 +729,11 @@ def test_stall_fp8(rank: int | None) -> None:
     """Test hook: in fp8_linear the producer of each cluster's CTA ``rank`` gives up (None: off; see
     include/gptq.h)."""
     _check(lib().gptq_test_stall_fp8(-1 if rank is None else int(rank)), "gptq_test_stall_fp8")
+
+
+def test_fp8_no_pair(on: bool) -> None:
+    """Test hook: fp8_linear without its kernel for pairs of CTAs (see include/gptq.h)."""
+    _check(lib().gptq_test_fp8_no_pair(int(bool(on))), "gptq_test_fp8_no_pair")
 
 
 def status_string(status: int) -> str:
