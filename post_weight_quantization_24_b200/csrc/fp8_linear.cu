@@ -10,13 +10,14 @@
 // kernel records GPTQ_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and returns. Tokens and
 // channels past the edges are zero-filled by TMA and not stored.
 //   fp8_pair_kernel    256 tokens x 256 channels per CTA pair, for calls with enough such tiles to
-//                      fill the GPU. 16384 tokens, 11008 -> 4096, fp16 with residual: 0.75 to 0.81
-//                      ms (1.8 to 2.0 PFLOP/s), 0.85 ms in long runs at the power limit, where
-//                      TMA and MMAs alone take 0.61 ms; without the promotion's multiply-adds
-//                      0.71 ms.
+//                      fill the GPU. 16384 tokens, 11008 -> 4096, fp16 with residual: 0.82 to 0.86
+//                      ms back to back (1.7 to 1.8 PFLOP/s), 0.77 ms in short runs. The
+//                      promotion's multiply-adds bound it: 1035 cycles per block at 1.52 GHz
+//                      with them; without them 690 to 740 at 1.30 to 1.41 GHz (0.63 ms, at the
+//                      power limit), as with TMA and MMAs alone.
 //   fp8_stream_kernel  128 channels x 16 to 128 tokens per CTA, the input channels split over a
 //                      cluster: for all other calls. 1 token, 4096 -> 4096: 7.2 us; 37 tokens,
-//                      11008 -> 4096, bf16 with residual: 15.5 us, about 4 us of them fixed
+//                      11008 -> 4096, bf16 with residual: 15.7 us, about 4 us of them fixed
 //                      (set-up, first loads, the join) and the rest at 4 to 5 TB/s of weights.
 #include <algorithm>
 #include <atomic>
@@ -61,7 +62,9 @@ gptq_status fp8_no_pair_set(int on) {
 }
 
 // NC accumulated columns of one row -> Y (+ R), value by value: for rows that do not all start on
-// 16-byte boundaries.
+// 16-byte boundaries. A warp's lanes are 32 rows, so each access touches 32 sectors for 64 or 128
+// useful bytes: 4096 tokens, 2048 -> 4095, fp16, take 201 us (242 with R) against 47 (53) for 2048 ->
+// 4096.
 template <typename T, int NC>
 __device__ __forceinline__ void f8_store(const F8Params& p, int row, int col0,
                                          const uint64_t (&acc)[NC / 2]) {
@@ -113,10 +116,10 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, con
 // stages and sends its partial sums to the CTAs that own their tokens (st.async into their shared
 // memory, counted on an mbarrier there), which add them in rank order, so equal inputs give equal
 // bits. Nobody reads another CTA's memory, so no cluster barrier (1100 cycles each) is left but
-// one whose latency the main loop covers: 16 tokens, 11008 -> 4096, 11.7 us against 12.9 with sums
-// read between two barriers. Two CTAs fit an SM, one for 128 tokens (128 tokens, 11008 -> 4096, took
-// 24 us with one of 6 stages, 31 us with two of 3). With tokens as M and no split the 37-token
-// call above took 43.6 us.
+// one whose latency the main loop covers: 16 tokens, 11008 -> 4096, took 11.7 us against 12.9 with
+// sums read between two barriers (11.4 now). Two CTAs fit an SM, one for 128 tokens (128 tokens, 11008
+// -> 4096, 17.5 us now, took 24 us with one of 6 stages, 31 us with two of 3, in an earlier form).
+// With tokens as M and no split the 37-token call above took 43.6 us.
 //   warp 0    TMA producer            warps 1, 2  MMA issuers, every other block each
 //   warps 3-  promotion: a thread owns one channel and EC tokens. The factors sx*sw (one per token
 //             and block) are put into shared memory for FBLK blocks at a time, which exposes
@@ -809,10 +812,10 @@ static gptq_status f8_launch(void (*kernel)(KArgs...), int grid, int cluster, in
 }
 
 // Ways to split the input channels of `tiles` streaming tiles, a power of two up to 8: until there is
-// a CTA for every SM, as long as each keeps 2 blocks (1 token, 1024 -> 1024: 4.6 us in quarters,
-// 4.9 us in halves). Where two CTAs share an SM, one more doubling pays if each keeps 8 blocks (37
-// tokens, 11008 -> 4096: 15.5 us in eighths, 17.1 us in quarters), and costs with fewer (64 tokens,
-// 4096 -> 4096: 11.3 us in eighths, 9.7 us in quarters).
+// a CTA for every SM, as long as each keeps 2 blocks (1 token, 1024 -> 1024: 3.8 us in quarters,
+// 4.6 us in halves). Where two CTAs share an SM, one more doubling pays if each keeps 8 blocks (37
+// tokens, 11008 -> 4096: 15.7 us in eighths, 17.0 us in quarters), and costs with fewer (64 tokens,
+// 4096 -> 4096: 10.7 us in eighths, 9.9 us in quarters).
 static int f8_splits(long long tiles, int n_kb, int per_sm) {
     int splits = 1;
     while (splits < 8 &&
@@ -921,10 +924,12 @@ static gptq_status fp8_linear_launch(const uint8_t* X8, const uint8_t* W8, F8Par
     const long long pair_tiles = static_cast<long long>((p.n_tok - 1) / f8p::PT + 1) *
                                  ((p.d_out - 1) / f8p::PT + 1);
     if (p.n_tok > 64) {
-        // Blocks of 128 input channels one after the other: a wave of pair tiles takes 0.5 us per
-        // block, a wave of 128 x 128 streaming tiles 0.6 us (measured at d_in 4096 and 11008), so
-        // the streaming kernel is taken where splitting d_in saves more than that (256 tokens,
-        // 11008 -> 4096: 31 us against 49 us; 256 tokens, 4096 -> 11008: 53 us against 23 us).
+        // Blocks of 128 input channels one after the other, a wave of pair tiles a little faster than
+        // one of 128 x 128 streaming tiles (0.55 and 0.53 to 0.6 us per block over 86 blocks, 0.68 us
+        // each over 32, start and end of the call included), so the streaming kernel is taken where
+        // splitting d_in or a partial wave saves more than the 5 to 6 of the rule. 256 tokens: 11008
+        // -> 4096 26 us, with pairs 49 us; 4096 -> 11008 42 us, with pairs 22 us. 384 tokens, 11008
+        // -> 4096: 45 us, with pairs, which the rule takes, 48 us.
         const long long pair_waves = (pair_tiles + num_sms() / 2 - 1) / (num_sms() / 2);
         const long long tiles = static_cast<long long>((p.n_tok - 1) / 128 + 1) * ((p.d_out - 1) / 128 + 1);
         const int splits = f8_splits(tiles, p.n_kb, 1);

@@ -10,8 +10,9 @@
 //
 // Both kernels read X once into registers and write its codes from there: bytes per value are
 // the input's 2 or 4 plus 1, plus the scales. They are bound by HBM: 16384 x 11008 bf16 activations
-// take 88 us (6.2 TB/s), 11008 x 4096 fp16 weights 21 us (6.3 TB/s), 4100 x 5136 fp32 weights 19
-// us (5.4 TB/s; 17 with one rounding and no bracket); a copy runs at 6.55 TB/s.
+// take 89 to 91 us (6.0 to 6.1 TB/s), fp32 146 us (6.2), 11008 x 4096 fp16 weights 24 us (5.6 TB/s; 22
+// where the codes find room in L2), 4100 x 5136 fp32 weights 19 to 20 us (5.3 TB/s; 17 with one
+// rounding and no bracket); a copy runs at 6.55 TB/s.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -59,7 +60,8 @@ static __device__ __noinline__ uint32_t codes_exact(float4 v, float a) {
 //   16-bit types: fma(v, r, v*r_lo) is the quotient within 2^-23 of itself, and the quotient itself
 //   where that is an fp32 number; with v and a of 11 bits it is a tie or 2^-17 off one.
 //   fp32: both ends of a bracket r (1 -+ 2^-22) (r and the products are within 2^-24) are rounded;
-//   where their codes differ (one value in 10^6) the exact decision is made.
+//   where their codes differ (one value in 200000, so four values in 50000, on normal data) the
+//   exact decision is made.
 template <typename T>
 __device__ __forceinline__ uint32_t codes4(const float* v, const Fp8Scale& f) {
     float p[4];
@@ -125,10 +127,10 @@ __device__ __forceinline__ void load32(const void* p, int wide, uint4* x) {
 
 // A CTA takes 8 tokens x 512 P channels. A warp takes one token: 8 lanes per 128-channel block, 16
 // consecutive values per lane (one store of 16 codes), 4 blocks per pass, P passes, all loads
-// first. The scales leave through shared memory as runs of 8 tokens. 16384 x 11008 bf16 takes 82 us
-// with P = 4, 86 with 2, 100 with 1; 94 with P = 2 and a lane's two vectors 128 bytes apart (8-byte
-// stores); 101 with 4 tokens x 128 channels per warp. The second multiply-add that makes the codes
-// exact then cost 6 us (two values per instruction: 13).
+// first. The scales leave through shared memory as runs of 8 tokens. 16384 x 11008 bf16 takes 91 us
+// with P = 4, 93 with 2, 119 with 1. Before the second multiply-add that makes the codes exact (6 us;
+// two values per instruction 13) these were 82, 86 and 100, and 94 with P = 2 and a lane's two
+// vectors 128 bytes apart (8-byte stores), 101 with 4 tokens x 128 channels per warp.
 template <typename T, int P>
 __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, int64_t n, int d,
                                                       uint8_t* __restrict__ codes,
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(256) fp8_act_kernel(const T* __restrict__ X, i
 // A CTA of 256 threads takes one 128 x 128 block, all of it in flight at once (32 KB of fp16): 8
 // lanes per row, whose 16-byte vectors lie 8 apart, 4 rows per warp and step. Registers are bounded
 // for three CTAs per SM with 16-bit inputs (with that, streaming loads and the overlapped launch
-// 26.5 us became 21; with 32-byte loads as above 24).
+// 26.5 us became 21, codes in L2; with 32-byte loads as above 24).
 template <typename T>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
     fp8_weight_kernel(const T* __restrict__ W, int d_out, int d_in, uint8_t* __restrict__ codes,
@@ -235,9 +237,9 @@ static gptq_status fp8_act_go(const void* X, int64_t n, int d, uint8_t* codes, f
 }
 
 // Passes per CTA: 2 KB of a row at a time in 16 bits, 4 KB where that leaves 16 CTAs for every SM
-// (16384 x 4096 fp16: 31.8 us, 32.9 with 2 KB; 2048 x 4096: 6.5 and 5.9), 1 KB where 2 KB leave fewer
-// than 4 (513 x 5136: 3.1 us, 3.3 with 2 KB). In fp32 no more than 4 KB (16384 x 11008: 8 KB took 6 % more).
-// The times are those before the codes were made exact.
+// (16384 x 4096 fp16: 34.9 us, 35.7 with 2 KB; 2048 x 4096: 6.7 and 5.9), 1 KB where 2 KB leave fewer
+// than 4 (513 x 5136: 2.6 us, 2.8 with 2 KB). In fp32 no more than 4 KB (16384 x 11008: 146 us, 156 with
+// 8 KB).
 template <typename T>
 static gptq_status fp8_act_launch(const void* X, int64_t n, int d, uint8_t* codes, float* scales,
                                   cudaStream_t s) {

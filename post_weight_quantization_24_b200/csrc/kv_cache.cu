@@ -3,9 +3,11 @@
 // read back as scale * (code - zero).
 //
 // Both kernels move each byte once. 16384 tokens x 32 heads x 128, 4 bits, bf16: writing takes 60 us
-// (5.7 TB/s, 0.87 of the copy rate), reading 60 us (5.8 TB/s); 131072 tokens x 8 heads x 128 read in
-// 114 us (6.0 TB/s, five bytes in six of them writes). A decode step's few tokens are bound by
-// launch latency (3 us on the device).
+// (5.7 TB/s, 0.87 of the copy rate), reading 59 us (5.8 TB/s); 131072 tokens x 8 heads x 128 read in
+// 113 us (6.1 TB/s, 78 % of the bytes are writes). Writing from fp32, 8 bits: 107 us (6.3 TB/s). Groups
+// of 16 write in 85 us (four sets of fp64 scalars per lane); rows that are no multiple of 256 elements
+// go pass by pass (16384 x 3 x 80: 13 us, 1.6 TB/s, read in 8). A decode step's few tokens are bound
+// by launch latency (3 us on the device).
 //
 // A token's heads lie together in the cache, so its n_heads * head_dim elements are one contiguous
 // row in every array: `wc` chunks of 8 elements, of which a warp takes 32 consecutive ones per
@@ -96,7 +98,8 @@ __device__ __noinline__ uint2 kv_codes_exact(float4 a, float4 b, float scale, fl
 //   For with v = m 2^a and scale = M 2^b (M < 2^11), a quotient other than k + 1/2 is off it by
 //   |2v - (2k+1) scale| / (2v) of itself, which is at least 2^min(a+1,b) / (2v): 2^-11 where a + 1
 //   < b, else 1 / (2 (k+1/2) M) > 2^-20 for k up to 255.
-//   fp32: the exact decision is made (one chunk in about 4000 for 4 bits, 300 for 8).
+//   fp32: the exact decision is made (one chunk in about 100000 for 4 bits, 6500 for 8, on normal
+//   data).
 // Ties are not rare: one warp's pass in seven has one in bf16, where the scales often end in
 // zeros (deciding them out of line took 4 % more).
 // The lower clamp is implied: rint(lo/s) + rint(-lo/s) = 0.
